@@ -44,6 +44,13 @@
  *     quotient in binary32 (correctly rounded), then rounded to the nearest
  *     code, ties to even, magnitudes beyond 448 saturating to 448. Reading
  *     uses code * scale. q, key, value and out stay bf16 or fp16.
+ *   - 8-bit caches with block scales: the *_fp8_block calls keep, instead of
+ *     one scale per cache, one float per (block, KV head) and cache, k_scales
+ *     and v_scales (device) [num_blocks, num_kv_heads], contiguous and
+ *     positive. pa_reshape_and_cache_fp8_block chooses them from the rows it
+ *     writes: 2^e with the smallest e >= -64 for which the block's largest
+ *     finite magnitude does not exceed 448 * 2^e. So a block uses the format's
+ *     range whatever its magnitudes are, and no scale has to be calibrated.
  *   - Supported now: head_dim 64, 80, 96, 128 or 256; block_size 8, 16 or 32 (the
  *     reading map, §2.3, sweeps page sizes; the kernels stage K/V 16 keys at a
  *     time); num_heads a multiple of num_kv_heads with group size 1, 2, 4 or 8.
@@ -290,6 +297,126 @@ pa_status pa_rope_reshape_and_cache_fp8(void *q, int64_t q_token_stride, const v
                                         int32_t num_tokens, int32_t num_heads, int32_t num_kv_heads,
                                         int32_t head_dim, int32_t block_size, int64_t num_blocks,
                                         float k_scale, float v_scale, int32_t dtype, void *stream);
+
+/*
+ * RMS norm of every query and key head, the rotation of
+ * pa_rope_reshape_and_cache, and the cache write, in one pass (out of place).
+ * For every token t with positions[t] in [0, max_position) and every head row
+ * x of q[t] or key[t]:
+ *   y = x * w / sqrt(mean(x^2) + eps)    (w: q_weight or k_weight, element i of
+ *                                         the head times w[i])
+ * and y is rotated as pa_rope_reshape_and_cache rotates (fp32 throughout, one
+ * rounding to the element type after both). q's rows go to q_out; if
+ * slot_mapping[t] >= 0, key's rows and value[t] unchanged go to the slot.
+ *   q_weight, k_weight (device): `dtype` [head_dim], 16-byte aligned; NULL
+ *       skips that norm (the row is rotated only). eps: finite and positive.
+ *   q_out (device): token t at q_out + t * q_out_token_stride elements (a
+ *       multiple of 8, >= num_heads * head_dim). Either q itself with q's
+ *       stride (in place) or rows that overlap no input.
+ *   head_dim a multiple of 8, at most 512. Every other argument, the skipped
+ *       tokens (out-of-range position: nothing written) and the flags as for
+ *       pa_rope_reshape_and_cache.
+ */
+pa_status pa_norm_rope_reshape_and_cache(const void *q, int64_t q_token_stride, const void *key, const void *value,
+                                         int64_t key_token_stride, int64_t value_token_stride,
+                                         const void *q_weight, const void *k_weight, float eps,
+                                         void *key_cache, void *value_cache, const int64_t *slot_mapping,
+                                         const int64_t *positions, const float *cos_sin_cache,
+                                         int32_t max_position, int32_t rotary_dim, int32_t is_neox,
+                                         int32_t num_tokens, int32_t num_heads, int32_t num_kv_heads,
+                                         int32_t head_dim, int32_t block_size, int64_t num_blocks,
+                                         void *q_out, int64_t q_out_token_stride, int32_t dtype, void *stream);
+
+/*
+ * The same into 8-bit caches with one scale per cache: key rows (rounded once
+ * to `dtype`) and value rows are stored as E4M3 codes of x / k_scale and
+ * x / v_scale, as pa_rope_reshape_and_cache_fp8 stores them (head_dim a
+ * multiple of 16, scales finite and positive).
+ */
+pa_status pa_norm_rope_reshape_and_cache_fp8(const void *q, int64_t q_token_stride, const void *key,
+                                             const void *value, int64_t key_token_stride,
+                                             int64_t value_token_stride, const void *q_weight,
+                                             const void *k_weight, float eps, void *key_cache, void *value_cache,
+                                             const int64_t *slot_mapping, const int64_t *positions,
+                                             const float *cos_sin_cache, int32_t max_position, int32_t rotary_dim,
+                                             int32_t is_neox, int32_t num_tokens, int32_t num_heads,
+                                             int32_t num_kv_heads, int32_t head_dim, int32_t block_size,
+                                             int64_t num_blocks, float k_scale, float v_scale, void *q_out,
+                                             int64_t q_out_token_stride, int32_t dtype, void *stream);
+
+/*
+ * The same norm and rotation without a cache: key's rows go to key_out (token
+ * stride key_out_token_stride; key itself with key's stride, or rows that
+ * overlap no input), ready for pa_reshape_and_cache_fp8_block.
+ */
+pa_status pa_norm_rope(const void *q, int64_t q_token_stride, const void *key, int64_t key_token_stride,
+                       const void *q_weight, const void *k_weight, float eps, const int64_t *positions,
+                       const float *cos_sin_cache, int32_t max_position, int32_t rotary_dim, int32_t is_neox,
+                       int32_t num_tokens, int32_t num_heads, int32_t num_kv_heads, int32_t head_dim,
+                       void *q_out, int64_t q_out_token_stride, void *key_out, int64_t key_out_token_stride,
+                       int32_t dtype, void *stream);
+
+/*
+ * reshape_and_cache into 8-bit caches with block scales. The new rows of
+ * request b are tokens [query_start_loc[b], query_start_loc[b + 1]) of key and
+ * value; they are its positions seq_lens[b] - query_len .. seq_lens[b] - 1 and
+ * go to those rows of the blocks its block-table row names (the arguments
+ * pa_attention_varlen_fp8_block takes next; slots are not passed because the
+ * call works block by block). Per (touched block, KV head), for K and for V:
+ *   needed = 2^e, the smallest e >= -64 with max |x| <= 448 * 2^e over the
+ *            block's new finite elements (2^-64 if there is none or all are 0);
+ *   scale  = needed, if the block's first row is among the new ones; else
+ *            max(scale, needed) with the scale the array holds (one that is
+ *            not positive and finite counts as 0);
+ *   a new element is stored as the E4M3 code of x / scale (rounded to nearest
+ *   even; infinities saturate, NaN gives a NaN code); if the scale grew, the
+ *   codes of the rows already there become E4M3(code * old / scale).
+ * Rows of a block at seq_len and beyond, and other blocks, are not touched.
+ * Two requests of one call must not write to the same block.
+ *   key, value, strides, caches: as for pa_reshape_and_cache_fp8.
+ *   k_scales, v_scales (device): float [num_blocks, num_kv_heads].
+ *   block_tables, seq_lens, query_start_loc, num_seqs, total_q_tokens,
+ *   max_query_len: as for pa_attention_varlen.
+ * Requests with contradicting lengths or a block id out of range are skipped
+ * and set PA_FLAG_LENGTHS, PA_FLAG_QUERY_LOC or PA_FLAG_BLOCK_RANGE.
+ */
+pa_status pa_reshape_and_cache_fp8_block(const void *key, const void *value, int64_t key_token_stride,
+                                         int64_t value_token_stride, void *key_cache, void *value_cache,
+                                         float *k_scales, float *v_scales, const int32_t *block_tables,
+                                         int32_t max_blocks_per_seq, const int32_t *seq_lens,
+                                         const int32_t *query_start_loc, int32_t num_seqs, int32_t total_q_tokens,
+                                         int32_t max_query_len, int32_t num_kv_heads, int32_t head_dim,
+                                         int32_t block_size, int64_t num_blocks, int32_t dtype, void *stream);
+
+/*
+ * Attention over 8-bit caches with block scales: pa_attention_varlen_fp8 with
+ * k_scales[block][kv_head] and v_scales[block][kv_head] in place of k_scale
+ * and v_scale (same workspace size):
+ *   out[t][h][:] = round( sum_j softmax_j(scale * q[t][h] . (ks_j * Kc[j]))
+ *                         * (vs_j * Vc[j]) ),  ks_j, vs_j of key j's block.
+ * Block scales that are read must be positive and finite. scale must be
+ * positive (PA_ERR_DIMS otherwise).
+ */
+pa_status pa_attention_varlen_fp8_block(const void *q, int64_t q_token_stride,
+                                        const void *key_cache, const void *value_cache,
+                                        const float *k_scales, const float *v_scales,
+                                        const int32_t *block_tables, int32_t max_blocks_per_seq,
+                                        const int32_t *seq_lens, const int32_t *query_start_loc,
+                                        int32_t num_seqs, int32_t total_q_tokens,
+                                        int32_t max_query_len, int32_t max_seq_len,
+                                        int32_t num_heads, int32_t num_kv_heads, int32_t head_dim,
+                                        int32_t block_size, int64_t num_blocks, float scale,
+                                        void *out, void *workspace, size_t workspace_bytes,
+                                        int32_t dtype, void *stream);
+
+/*
+ * The scales' part of a copy-on-write copy of 8-bit blocks with block scales:
+ * for each pair i, k_scales[dst] = k_scales[src] and v_scales[dst] =
+ * v_scales[src], all heads (pa_copy_blocks copies the codes). block_mapping
+ * and its rules as for pa_copy_blocks.
+ */
+pa_status pa_copy_block_scales(float *k_scales, float *v_scales, const int64_t *block_mapping,
+                               int32_t num_pairs, int32_t num_kv_heads, int64_t num_blocks, void *stream);
 
 /*
  * Copy-on-write block copy (LLM-infra reading map, §2.2: a physical block

@@ -200,13 +200,14 @@ pa_status pa_attention_plan_info(int32_t num_seqs, int32_t max_seq_len, int32_t 
 
 namespace {
 
-// pa_attention_varlen and pa_attention_varlen_fp8: validation, then the launch.
+// pa_attention_varlen and its 8-bit forms: validation, then the launch.
+// k_scales (with v_scales): block scales in place of k_scale and v_scale.
 pa_status attention_call(const void *q, int64_t q_token_stride, const void *key_cache, const void *value_cache,
                          const int32_t *block_tables, int32_t max_blocks_per_seq, const int32_t *seq_lens,
                          const int32_t *query_start_loc, int32_t num_seqs, int32_t total_q_tokens,
                          int32_t max_query_len, int32_t max_seq_len, int32_t num_heads, int32_t num_kv_heads,
                          int32_t head_dim, int32_t block_size, int64_t num_blocks, float scale, bool kv_fp8,
-                         float k_scale, float v_scale, void *out, void *workspace, size_t workspace_bytes,
+                         float k_scale, float v_scale, const float *k_scales, const float *v_scales, void *out, void *workspace, size_t workspace_bytes,
                          int32_t dtype, void *stream) {
   cudaEvent_t ev_start = t_ev_start, ev_stop = t_ev_stop, tile_start = t_tile_start, tile_stop = t_tile_stop;
   t_ev_start = t_ev_stop = t_tile_start = t_tile_stop = nullptr;
@@ -262,6 +263,8 @@ pa_status attention_call(const void *q, int64_t q_token_stride, const void *key_
   a.kv_fp8 = kv_fp8;
   a.k_scale = kv_fp8 ? k_scale : 1.0f;
   a.v_scale = kv_fp8 ? v_scale : 1.0f;
+  a.k_scales = k_scales;
+  a.v_scales = v_scales;
   a.out = out;
   a.workspace = workspace;
   a.status = ds->status;
@@ -290,8 +293,8 @@ pa_status pa_attention_varlen(const void *q, int64_t q_token_stride, const void 
                               size_t workspace_bytes, int32_t dtype, void *stream) {
   return attention_call(q, q_token_stride, key_cache, value_cache, block_tables, max_blocks_per_seq, seq_lens,
                         query_start_loc, num_seqs, total_q_tokens, max_query_len, max_seq_len, num_heads,
-                        num_kv_heads, head_dim, block_size, num_blocks, scale, false, 1.0f, 1.0f, out, workspace,
-                        workspace_bytes, dtype, stream);
+                        num_kv_heads, head_dim, block_size, num_blocks, scale, false, 1.0f, 1.0f, nullptr, nullptr,
+                        out, workspace, workspace_bytes, dtype, stream);
 }
 
 pa_status pa_attention_varlen_fp8(const void *q, int64_t q_token_stride, const void *key_cache,
@@ -303,8 +306,27 @@ pa_status pa_attention_varlen_fp8(const void *q, int64_t q_token_stride, const v
                                   void *workspace, size_t workspace_bytes, int32_t dtype, void *stream) {
   return attention_call(q, q_token_stride, key_cache, value_cache, block_tables, max_blocks_per_seq, seq_lens,
                         query_start_loc, num_seqs, total_q_tokens, max_query_len, max_seq_len, num_heads,
-                        num_kv_heads, head_dim, block_size, num_blocks, scale, true, k_scale, v_scale, out,
-                        workspace, workspace_bytes, dtype, stream);
+                        num_kv_heads, head_dim, block_size, num_blocks, scale, true, k_scale, v_scale, nullptr, nullptr,
+                        out, workspace, workspace_bytes, dtype, stream);
+}
+
+pa_status pa_attention_varlen_fp8_block(const void *q, int64_t q_token_stride, const void *key_cache,
+                                        const void *value_cache, const float *k_scales, const float *v_scales,
+                                        const int32_t *block_tables, int32_t max_blocks_per_seq,
+                                        const int32_t *seq_lens, const int32_t *query_start_loc, int32_t num_seqs,
+                                        int32_t total_q_tokens, int32_t max_query_len, int32_t max_seq_len,
+                                        int32_t num_heads, int32_t num_kv_heads, int32_t head_dim,
+                                        int32_t block_size, int64_t num_blocks, float scale, void *out,
+                                        void *workspace, size_t workspace_bytes, int32_t dtype, void *stream) {
+  if (!(scale > 0.0f)) return PA_ERR_DIMS;
+  if (num_seqs > 0 && total_q_tokens > 0) {
+    if (!k_scales || !v_scales) return PA_ERR_NULL;
+    if (!aligned(k_scales, 4) || !aligned(v_scales, 4)) return PA_ERR_ALIGN;
+  }
+  return attention_call(q, q_token_stride, key_cache, value_cache, block_tables, max_blocks_per_seq, seq_lens,
+                        query_start_loc, num_seqs, total_q_tokens, max_query_len, max_seq_len, num_heads,
+                        num_kv_heads, head_dim, block_size, num_blocks, scale, true, 1.0f, 1.0f, k_scales, v_scales,
+                        out, workspace, workspace_bytes, dtype, stream);
 }
 
 }  // extern "C"
@@ -353,7 +375,221 @@ pa_status rope_call(void *q, int64_t q_token_stride, const void *key, const void
 
 }  // namespace
 
+namespace {
+
+// pa_norm_rope and its cache forms (dst 0 K rows, 1 16-bit caches, 2 8-bit
+// caches): validation, then the launch. The caller has filled in `p`.
+pa_status norm_rope_call(pa::NormRopeLaunch &p, int32_t block_size, int64_t num_blocks, void *stream) {
+  const bool cached = p.dst != 0, kv8 = p.dst == 2;
+  if (p.dtype != PA_BF16 && p.dtype != PA_FP16) return PA_ERR_UNSUPPORTED;
+  if (p.num_tokens < 0 || p.num_heads <= 0 || p.num_kv_heads <= 0 || p.head_dim <= 0 || p.max_position <= 0 ||
+      p.rotary_dim <= 0 || p.rotary_dim > p.head_dim || (cached && (block_size <= 0 || num_blocks < 0)))
+    return PA_ERR_DIMS;
+  if (!std::isfinite(p.eps) || !(p.eps > 0.0f)) return PA_ERR_DIMS;
+  if (kv8 && (!valid_cache_scale(p.k_scale) || !valid_cache_scale(p.v_scale))) return PA_ERR_DIMS;
+  if (p.head_dim % (kv8 ? 16 : 8) || p.rotary_dim % 16) return PA_ERR_ALIGN;
+  if (p.head_dim > 512) return PA_ERR_UNSUPPORTED;  // a head row is at most one warp's
+  // a token's q, K and V rows, counted in 16-byte chunks, are an int32 in the kernel
+  if ((static_cast<int64_t>(p.num_heads) + 2 * static_cast<int64_t>(p.num_kv_heads)) * (p.head_dim / 8) > INT32_MAX)
+    return PA_ERR_UNSUPPORTED;
+  if (cached && num_blocks > INT64_MAX / block_size) return PA_ERR_UNSUPPORTED;
+  if (p.num_tokens == 0) return PA_OK;
+  if (!p.q || !p.key || !p.q_out || !p.key_dst || !p.positions || !p.cos_sin) return PA_ERR_NULL;
+  if (cached && (!p.value || !p.value_dst || !p.slot_mapping)) return PA_ERR_NULL;
+  const int64_t q_row = static_cast<int64_t>(p.num_heads) * p.head_dim;
+  const int64_t kv_row = static_cast<int64_t>(p.num_kv_heads) * p.head_dim;
+  if (p.q_stride < q_row || p.q_out_stride < q_row || p.key_stride < kv_row) return PA_ERR_DIMS;
+  if (cached ? p.value_stride < kv_row : p.key_out_stride < kv_row) return PA_ERR_DIMS;
+  // in place means row for row
+  if (p.q_out == p.q && p.q_out_stride != p.q_stride) return PA_ERR_DIMS;
+  if (!cached && p.key_dst == p.key && p.key_out_stride != p.key_stride) return PA_ERR_DIMS;
+  if (p.q_stride % 8 || p.q_out_stride % 8 || p.key_stride % 8 || p.value_stride % 8 || p.key_out_stride % 8)
+    return PA_ERR_ALIGN;
+  if (!aligned(p.q, 16) || !aligned(p.key, 16) || !aligned(p.value, 16) || !aligned(p.q_out, 16) ||
+      !aligned(p.key_dst, 16) || !aligned(p.value_dst, 16) || !aligned(p.q_weight, 16) || !aligned(p.k_weight, 16) ||
+      !aligned(p.cos_sin, 16) || !aligned(p.slot_mapping, 8) || !aligned(p.positions, 8))
+    return PA_ERR_ALIGN;
+  DeviceState *ds = device_state();
+  if (!ds) return PA_ERR_CUDA;
+  p.num_slots = cached ? num_blocks * block_size : 0;
+  p.status = ds->status;
+  const cudaError_t err = pa::launch_norm_rope(p, ds->sm_count, static_cast<cudaStream_t>(stream));
+  if (err != cudaSuccess) return cuda_failure(PA_ERR_LAUNCH, err);
+  g_launches.fetch_add(1);
+  return PA_OK;
+}
+
+pa::NormRopeLaunch norm_rope_args(const void *q, int64_t q_token_stride, const void *key, int64_t key_token_stride,
+                                  const void *q_weight, const void *k_weight, float eps, const int64_t *positions,
+                                  const float *cos_sin_cache, int32_t max_position, int32_t rotary_dim,
+                                  int32_t is_neox, int32_t num_tokens, int32_t num_heads, int32_t num_kv_heads,
+                                  int32_t head_dim, void *q_out, int64_t q_out_token_stride, int32_t dtype) {
+  pa::NormRopeLaunch p = {};
+  p.q = q;
+  p.q_stride = q_token_stride;
+  p.key = key;
+  p.key_stride = key_token_stride;
+  p.q_weight = q_weight;
+  p.k_weight = k_weight;
+  p.eps = eps;
+  p.positions = positions;
+  p.cos_sin = cos_sin_cache;
+  p.max_position = max_position;
+  p.rotary_dim = rotary_dim;
+  p.is_neox = is_neox != 0;
+  p.num_tokens = num_tokens;
+  p.num_heads = num_heads;
+  p.num_kv_heads = num_kv_heads;
+  p.head_dim = head_dim;
+  p.q_out = q_out;
+  p.q_out_stride = q_out_token_stride;
+  p.k_scale = p.v_scale = 1.0f;
+  p.dtype = dtype;
+  return p;
+}
+
+}  // namespace
+
 extern "C" {
+
+pa_status pa_norm_rope_reshape_and_cache(const void *q, int64_t q_token_stride, const void *key, const void *value,
+                                         int64_t key_token_stride, int64_t value_token_stride, const void *q_weight,
+                                         const void *k_weight, float eps, void *key_cache, void *value_cache,
+                                         const int64_t *slot_mapping, const int64_t *positions,
+                                         const float *cos_sin_cache, int32_t max_position, int32_t rotary_dim,
+                                         int32_t is_neox, int32_t num_tokens, int32_t num_heads,
+                                         int32_t num_kv_heads, int32_t head_dim, int32_t block_size,
+                                         int64_t num_blocks, void *q_out, int64_t q_out_token_stride, int32_t dtype,
+                                         void *stream) {
+  pa::NormRopeLaunch p =
+      norm_rope_args(q, q_token_stride, key, key_token_stride, q_weight, k_weight, eps, positions, cos_sin_cache,
+                     max_position, rotary_dim, is_neox, num_tokens, num_heads, num_kv_heads, head_dim, q_out,
+                     q_out_token_stride, dtype);
+  p.value = value;
+  p.value_stride = value_token_stride;
+  p.key_dst = key_cache;
+  p.value_dst = value_cache;
+  p.slot_mapping = slot_mapping;
+  p.dst = 1;
+  return norm_rope_call(p, block_size, num_blocks, stream);
+}
+
+pa_status pa_norm_rope_reshape_and_cache_fp8(const void *q, int64_t q_token_stride, const void *key,
+                                             const void *value, int64_t key_token_stride,
+                                             int64_t value_token_stride, const void *q_weight, const void *k_weight,
+                                             float eps, void *key_cache, void *value_cache,
+                                             const int64_t *slot_mapping, const int64_t *positions,
+                                             const float *cos_sin_cache, int32_t max_position, int32_t rotary_dim,
+                                             int32_t is_neox, int32_t num_tokens, int32_t num_heads,
+                                             int32_t num_kv_heads, int32_t head_dim, int32_t block_size,
+                                             int64_t num_blocks, float k_scale, float v_scale, void *q_out,
+                                             int64_t q_out_token_stride, int32_t dtype, void *stream) {
+  pa::NormRopeLaunch p =
+      norm_rope_args(q, q_token_stride, key, key_token_stride, q_weight, k_weight, eps, positions, cos_sin_cache,
+                     max_position, rotary_dim, is_neox, num_tokens, num_heads, num_kv_heads, head_dim, q_out,
+                     q_out_token_stride, dtype);
+  p.value = value;
+  p.value_stride = value_token_stride;
+  p.key_dst = key_cache;
+  p.value_dst = value_cache;
+  p.slot_mapping = slot_mapping;
+  p.k_scale = k_scale;
+  p.v_scale = v_scale;
+  p.dst = 2;
+  return norm_rope_call(p, block_size, num_blocks, stream);
+}
+
+pa_status pa_norm_rope(const void *q, int64_t q_token_stride, const void *key, int64_t key_token_stride,
+                       const void *q_weight, const void *k_weight, float eps, const int64_t *positions,
+                       const float *cos_sin_cache, int32_t max_position, int32_t rotary_dim, int32_t is_neox,
+                       int32_t num_tokens, int32_t num_heads, int32_t num_kv_heads, int32_t head_dim, void *q_out,
+                       int64_t q_out_token_stride, void *key_out, int64_t key_out_token_stride, int32_t dtype,
+                       void *stream) {
+  pa::NormRopeLaunch p =
+      norm_rope_args(q, q_token_stride, key, key_token_stride, q_weight, k_weight, eps, positions, cos_sin_cache,
+                     max_position, rotary_dim, is_neox, num_tokens, num_heads, num_kv_heads, head_dim, q_out,
+                     q_out_token_stride, dtype);
+  p.key_dst = key_out;
+  p.key_out_stride = key_out_token_stride;
+  return norm_rope_call(p, 0, 0, stream);
+}
+
+pa_status pa_reshape_and_cache_fp8_block(const void *key, const void *value, int64_t key_token_stride,
+                                         int64_t value_token_stride, void *key_cache, void *value_cache,
+                                         float *k_scales, float *v_scales, const int32_t *block_tables,
+                                         int32_t max_blocks_per_seq, const int32_t *seq_lens,
+                                         const int32_t *query_start_loc, int32_t num_seqs, int32_t total_q_tokens,
+                                         int32_t max_query_len, int32_t num_kv_heads, int32_t head_dim,
+                                         int32_t block_size, int64_t num_blocks, int32_t dtype, void *stream) {
+  if (dtype != PA_BF16 && dtype != PA_FP16) return PA_ERR_UNSUPPORTED;
+  if (num_seqs < 0 || total_q_tokens < 0 || max_query_len < 0 || max_blocks_per_seq < 0 || num_kv_heads <= 0 ||
+      head_dim <= 0 || block_size <= 0 || num_blocks < 0)
+    return PA_ERR_DIMS;
+  if (!supported_head_dim(head_dim)) return PA_ERR_UNSUPPORTED;
+  if (block_size != 8 && block_size != 16 && block_size != 32) return PA_ERR_UNSUPPORTED;
+  const int64_t row = static_cast<int64_t>(num_kv_heads) * head_dim;
+  if (row > INT32_MAX) return PA_ERR_UNSUPPORTED;  // a token row's element count is an int32 in the kernel
+  if (num_seqs == 0 || total_q_tokens == 0) return PA_OK;
+  if (max_query_len == 0 || max_query_len > total_q_tokens || max_blocks_per_seq == 0 || num_blocks == 0)
+    return PA_ERR_DIMS;
+  // one warp per (unit, KV head, K or V), eight to a CTA of a 31-bit grid
+  const int64_t units = total_q_tokens / block_size + 2 * static_cast<int64_t>(num_seqs);
+  if (units > INT32_MAX || units > (static_cast<int64_t>(INT32_MAX) - 1) * 8 / (2 * static_cast<int64_t>(num_kv_heads)))
+    return PA_ERR_UNSUPPORTED;
+  if (!key || !value || !key_cache || !value_cache || !k_scales || !v_scales || !block_tables || !seq_lens ||
+      !query_start_loc)
+    return PA_ERR_NULL;
+  if (key_token_stride < row || value_token_stride < row) return PA_ERR_DIMS;
+  if (key_token_stride % 8 || value_token_stride % 8) return PA_ERR_ALIGN;
+  if (!aligned(key, 16) || !aligned(value, 16) || !aligned(key_cache, 16) || !aligned(value_cache, 16) ||
+      !aligned(k_scales, 4) || !aligned(v_scales, 4) || !aligned(block_tables, 4) || !aligned(seq_lens, 4) ||
+      !aligned(query_start_loc, 4))
+    return PA_ERR_ALIGN;
+  DeviceState *ds = device_state();
+  if (!ds) return PA_ERR_CUDA;
+  pa::BlockScatterLaunch p = {};
+  p.key = key;
+  p.value = value;
+  p.key_stride = key_token_stride;
+  p.value_stride = value_token_stride;
+  p.key_cache = key_cache;
+  p.value_cache = value_cache;
+  p.k_scales = k_scales;
+  p.v_scales = v_scales;
+  p.block_tables = block_tables;
+  p.max_blocks_per_seq = max_blocks_per_seq;
+  p.seq_lens = seq_lens;
+  p.query_start_loc = query_start_loc;
+  p.num_seqs = num_seqs;
+  p.total_q = total_q_tokens;
+  p.max_query_len = max_query_len;
+  p.num_kv_heads = num_kv_heads;
+  p.head_dim = head_dim;
+  p.block_size = block_size;
+  p.num_blocks = num_blocks;
+  p.dtype = dtype;
+  p.status = ds->status;
+  const cudaError_t err = pa::launch_block_scatter(p, ds->sm_count, static_cast<cudaStream_t>(stream));
+  if (err != cudaSuccess) return cuda_failure(PA_ERR_LAUNCH, err);
+  g_launches.fetch_add(1);
+  return PA_OK;
+}
+
+pa_status pa_copy_block_scales(float *k_scales, float *v_scales, const int64_t *block_mapping, int32_t num_pairs,
+                               int32_t num_kv_heads, int64_t num_blocks, void *stream) {
+  if (num_pairs < 0 || num_kv_heads <= 0 || num_blocks < 0) return PA_ERR_DIMS;
+  if (num_pairs == 0) return PA_OK;
+  if (!k_scales || !v_scales || !block_mapping) return PA_ERR_NULL;
+  if (!aligned(k_scales, 4) || !aligned(v_scales, 4) || !aligned(block_mapping, 8)) return PA_ERR_ALIGN;
+  DeviceState *ds = device_state();
+  if (!ds) return PA_ERR_CUDA;
+  const cudaError_t err =
+      pa::launch_copy_block_scales(k_scales, v_scales, block_mapping, num_pairs, num_kv_heads, num_blocks, ds->status,
+                                   ds->sm_count, static_cast<cudaStream_t>(stream));
+  if (err != cudaSuccess) return cuda_failure(PA_ERR_LAUNCH, err);
+  g_launches.fetch_add(1);
+  return PA_OK;
+}
 
 pa_status pa_rope_reshape_and_cache(void *q, int64_t q_token_stride, const void *key, const void *value,
                                     int64_t key_token_stride, int64_t value_token_stride, void *key_cache,

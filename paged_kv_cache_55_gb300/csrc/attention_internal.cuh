@@ -40,16 +40,19 @@ struct TileParams {
   int32_t num_seqs;
   int32_t total_q;
   int32_t max_tiles;
+  const float *k_scales;  // 8-bit caches with block scales: [num_blocks][Hkv]
+  const float *v_scales;
   unsigned int *status;
 };
 
 // Enqueue the tensor-core prefill-tile kernel (PDL launch) on `stream`; E is
 // the element type of q and out (ElemBf16 or ElemFp16); KV8: the caches hold
 // 8-bit E4M3 codes (the maps then have one-byte elements and boxes of
-// min(block_size, 32) rows of head_dim codes).
+// min(block_size, 32) rows of head_dim codes); BSC: with a scale per (block,
+// KV head) instead of one per cache.
 // vmapb: at head_dim 128 over 16-bit caches, the value cache as whole-block
 // boxes (block_size rows x both 64-element atoms; unused otherwise).
-template <int D, int G, typename E, bool KV8>
+template <int D, int G, typename E, bool KV8, bool BSC>
 cudaError_t launch_prefill_tiles(const CUtensorMap &kmap, const CUtensorMap &vmap, const CUtensorMap &vmapb,
                                  const TileParams &tp, int sm_count, cudaStream_t stream);
 

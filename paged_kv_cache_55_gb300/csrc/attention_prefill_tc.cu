@@ -74,6 +74,9 @@ constexpr int kParts = 2;        // softmax warps per TMEM lane quadrant and hal
 constexpr int kKeyTile = 128;    // keys per range (UMMA N of S, K of P V)
 constexpr int kMaxSlots = 8;     // K/V ring slots (as many as shared memory holds)
 constexpr int kUnitSlots = 2;    // published unit records
+// Block scales of a range, per 8-key group: K's scale and log2 of V's (8-bit caches with block scales).
+constexpr int kScaleSlotBytes = kKeyTile / 8 * 8;
+constexpr int kScaleSlotsMax = kMaxSlots / 2 + 1;
 // Warp roles. The MMA warp is warp 0: its issue rate sets the tensor cores'
 // (they queue only a couple of products) and it shares a scheduler with
 // softmax warps; the schedulers favour lower-numbered warps when several are
@@ -122,13 +125,22 @@ struct TcLayout {
   static constexpr int B_FULL = 0, B_EMPTY = kMaxSlots, B_RAW = 2 * kMaxSlots, B_CONV = 3 * kMaxSlots;
   static constexpr int B_S = 4 * kMaxSlots, B_P = B_S + kHalves, B_O = B_P + kHalves, B_QF = B_O + kHalves;
   static constexpr int B_QE = B_QF + kHalves, B_UF = B_QE + kHalves, B_UE = B_UF + kUnitSlots;
-  static constexpr int B_X = B_UE + kUnitSlots, B_DRAIN = B_X + 4 * kHalves, NBARS = B_DRAIN + 1;
+  static constexpr int B_X = B_UE + kUnitSlots, B_DRAIN = B_X + 4 * kHalves, B_SC = B_DRAIN + 1;
+  static constexpr int NBARS = B_SC + kScaleSlotsMax;  // sc: a range's block scales are in shared memory
   static constexpr int XCH_BYTES = kHalves * kParts * kHalfRows * 4;  // one float per (half, part, row)
   static constexpr int UNIT_BYTES = kUnitSlots * 32;                  // records of eight ints
   static constexpr int VF_BYTES = kMaxSlots * 8;                      // per V range and converter warp: kept bf16
   static constexpr int FIXED = kHalves * Q_BYTES + XCH_BYTES + UNIT_BYTES + VF_BYTES + 8 * NBARS + 16;
   static constexpr int FIT = (227 * 1024 - FIXED) / KV_BYTES;
   static constexpr int SLOTS = FIT < kMaxSlots ? FIT : kMaxSlots;
+  // Block scales of a range (scale_slot_bytes), SCALE_SLOTS of them in turn.
+  // The producer writes range g's once the ring slot of K(g) is free, that is,
+  // once load 2 g - SLOTS has been used up: V of range g - (SLOTS + 1) / 2 (odd
+  // SLOTS; its P is written) or K of range g - SLOTS / 2 (even; S of a range
+  // is issued only after both halves' P of the range before it). So the
+  // softmax warps have finished with range g - SCALE_SLOTS.
+  static constexpr int SCALE_SLOTS = SLOTS / 2 + 1;
+  static_assert(SCALE_SLOTS <= kScaleSlotsMax, "a barrier per scale slot");
   static_assert(SLOTS >= 4, "the ring holds at least K and V of two ranges");
   static constexpr int Q_OFF = 0;                                // Q of halves A and B
   static constexpr int RING_OFF = Q_OFF + kHalves * Q_BYTES;     // K(0), V(0), K(1), V(1), ... in SLOTS slots
@@ -137,7 +149,8 @@ struct TcLayout {
   static constexpr int VF_OFF = UNIT_OFF + UNIT_BYTES;           // V range flags (bf16 V rewritten as fp16)
   static constexpr int BAR_OFF = VF_OFF + VF_BYTES;
   static constexpr int TMEM_OFF = BAR_OFF + 8 * NBARS;
-  static constexpr int BYTES = TMEM_OFF + 16;
+  static constexpr int SC_OFF = TMEM_OFF + 16;
+  static constexpr int BYTES = SC_OFF + SCALE_SLOTS * kScaleSlotBytes;
   // Shared memory requested per CTA: more than half an SM's, so that a second
   // CTA (which would wait for TMEM) never lands on the same SM.
   static constexpr int REQUEST = BYTES > 116 * 1024 ? BYTES : 116 * 1024;
@@ -188,6 +201,16 @@ __device__ __forceinline__ void mma_ts(uint32_t d_tmem, uint32_t a_tmem, uint32_
       " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], b, %4, p;\n}\n" ::"r"(d_tmem),
       "r"(a_tmem), "r"(b_lo), "r"(b_hi), "r"(idesc), "n"(ACC)
       : "memory");
+}
+
+// Block scales of two neighbouring 8-key groups: (K scale, log2 V scale) of each.
+__device__ __forceinline__ float4 ld_scales(uint32_t addr) {
+  float4 v;
+  asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];\n"
+               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+               : "r"(addr)
+               : "memory");
+  return v;
 }
 
 // 32 consecutive 32-bit columns of this thread's TMEM lane; the wait is in
@@ -254,6 +277,31 @@ __device__ __forceinline__ float masked_max32(const uint32_t (&s)[32], int ck0, 
   return m;
 }
 
+// Row maximum of 32 scores under block scales: s * (sl2 * ks) + lv of each
+// 8-key group (scale pairs at shared address sc), as separately rounded
+// operations. ks and sl2 are positive, so a group's largest raw score gives
+// its largest scaled one.
+__device__ __forceinline__ float scaled_max32(const uint32_t (&s)[32], int ck0, int lim, float sl2, uint32_t sc) {
+  const float4 c01 = ld_scales(sc), c23 = ld_scales(sc + 16);
+  const float ks[4] = {c01.x, c01.z, c23.x, c23.z}, lv[4] = {c01.y, c01.w, c23.y, c23.w};
+  float m = -INFINITY;
+#pragma unroll
+  for (int g = 0; g < 4; ++g) {
+    float t;
+    if (ck0 + 32 <= lim) {
+      t = max3(max3(__uint_as_float(s[8 * g]), __uint_as_float(s[8 * g + 1]), __uint_as_float(s[8 * g + 2])),
+               max3(__uint_as_float(s[8 * g + 3]), __uint_as_float(s[8 * g + 4]), __uint_as_float(s[8 * g + 5])),
+               fmaxf(__uint_as_float(s[8 * g + 6]), __uint_as_float(s[8 * g + 7])));
+    } else {
+      t = -INFINITY;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) t = ck0 + 8 * g + i < lim ? fmaxf(t, __uint_as_float(s[8 * g + i])) : t;
+    }
+    m = fmaxf(m, __fadd_rn(__fmul_rn(t, __fmul_rn(sl2, ks[g])), lv[g]));
+  }
+  return m;
+}
+
 // Store 8 32-bit columns (raw bits) of this thread's TMEM lane.
 __device__ __forceinline__ void tmem_st8u(uint32_t taddr, const uint32_t (&v)[8]) {
   asm volatile(
@@ -309,6 +357,45 @@ __device__ __forceinline__ void probs16_store(const uint32_t *s, int k0, int lim
   if (SPLIT) tmem_st8u(col + 8, lv);
 }
 
+// The same for 16 keys under block scales, one fp16 P per key: the first and
+// the last eight keys have scale pairs (K scale ks, lv = log2 V scale) at
+// shared address sc. P' = 2^(s * sl2 * ks + lv - ms) carries the V scale, so O
+// accumulates P' times codes; the row sum takes P' / 2^lv.
+template <bool EXACT>
+__device__ __forceinline__ void probs16_scaled_store(const uint32_t *s, int k0, int lim, float sl2, float ms,
+                                                     float &sum, uint32_t col, uint32_t sc) {
+  const bool full = k0 + 16 <= lim;
+  const float4 c = ld_scales(sc);
+  const float f[2] = {__fmul_rn(sl2, c.x), __fmul_rn(sl2, c.z)}, lv[2] = {c.y, c.w};
+  uint32_t hv[8];
+#pragma unroll
+  for (int g = 0; g < 2; ++g) {
+    const float add = lv[g] - ms;
+    float acc0 = 0.f, acc1 = 0.f;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const int i = 4 * g + j;
+      float x0 = __uint_as_float(s[2 * i]), x1 = __uint_as_float(s[2 * i + 1]);
+      if (!full) {
+        x0 = k0 + 2 * i < lim ? x0 : -INFINITY;
+        x1 = k0 + 2 * i + 1 < lim ? x1 : -INFINITY;
+      }
+      float e0, e1;
+      if (EXACT) {
+        e0 = __fsub_rn(__fadd_rn(__fmul_rn(x0, f[g]), lv[g]), ms);
+        e1 = __fsub_rn(__fadd_rn(__fmul_rn(x1, f[g]), lv[g]), ms);
+      } else {
+        fma2(e0, e1, x0, x1, f[g], f[g], add, add);
+      }
+      const float p0 = ex2_approx(e0), p1 = ex2_approx(e1);
+      add2(acc0, acc1, acc0, acc1, p0, p1);
+      hv[i] = ElemFp16::pack(p0, p1);
+    }
+    sum = fmaf(acc0 + acc1, ex2_approx(-lv[g]), sum);
+  }
+  tmem_st8u(col, hv);
+}
+
 // P of one softmax warp's 64 keys of a range, from column sp of its lane,
 // the scores read again from TMEM 32 at a time (P of the first 32 keys never
 // covers the columns of the second). PAIR: a bf16 hi + lo pair per key, 16
@@ -352,6 +439,22 @@ __device__ __forceinline__ void tmem_ld32x2_wait(uint32_t taddr, uint32_t (&a)[3
       : "=r"(b[0]), "=r"(b[1]), "=r"(b[2]), "=r"(b[3]), "=r"(b[4]), "=r"(b[5]), "=r"(b[6]), "=r"(b[7]), "=r"(b[8]), "=r"(b[9]), "=r"(b[10]), "=r"(b[11]), "=r"(b[12]), "=r"(b[13]), "=r"(b[14]), "=r"(b[15]), "=r"(b[16]), "=r"(b[17]), "=r"(b[18]), "=r"(b[19]), "=r"(b[20]), "=r"(b[21]), "=r"(b[22]), "=r"(b[23]), "=r"(b[24]), "=r"(b[25]), "=r"(b[26]), "=r"(b[27]), "=r"(b[28]), "=r"(b[29]), "=r"(b[30]), "=r"(b[31])
       : "r"(taddr + 32)
       : "memory");
+}
+
+// Block scales of the 8-key group that starts at `key` (this KV head); left as
+// they are past the last key or for a block id out of range. p.k_scales and
+// p.v_scales may have been written shortly before: not an invariant load.
+__device__ __forceinline__ void block_scales_of(const TileParams &p, const int32_t *table, int key, int kv_end, int kvh,
+                                                float &ks, float &vs) {
+  if (key >= kv_end) return;
+  const int phys = __ldg(table + (key >> p.block_shift));
+  if (phys < 0 || phys >= p.num_blocks) return;
+  const int64_t at = static_cast<int64_t>(phys) * p.num_kv_heads + kvh;
+  ks = ld_cg(p.k_scales + at);
+  vs = ld_cg(p.v_scales + at);
+}
+__device__ __forceinline__ void st_scales(uint32_t addr, float ks, float lv) {
+  asm volatile("st.shared.v2.f32 [%0], {%1, %2};\n" ::"r"(addr), "f"(ks), "f"(lv) : "memory");
 }
 
 // A published unit: a tile of one request and one KV head, or the end of the stream.
@@ -444,7 +547,11 @@ __device__ __forceinline__ void vrange_back_to_bf16(uint32_t sV, int c0, int nva
 // bf16 and its flags send the softmax warps and the MMA warp to the hi + lo
 // pair for that range. Either way the rows past the unit's last key are
 // zeroed.
-template <int D, int G, typename E, bool KV8>
+//
+// With block scales (BSC) the producer also stages each range's scales, one
+// pair (K scale, log2 V scale) per 8-key group, which the softmax warps fold
+// into the exponents as the decode kernel does (probs16_scaled_store).
+template <int D, int G, typename E, bool KV8, bool BSC>
 // Twenty warps (two of them idle over fp16 caches), one CTA per SM.
 __global__ void __launch_bounds__(KV8 ? kTileThreads8 : kTileThreads, 1)
     prefill_tile_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap,
@@ -517,6 +624,7 @@ __global__ void __launch_bounds__(KV8 ? kTileThreads8 : kTileThreads, 1)
       mbar_init(bar(Lay::B_UE + i), 1 + kSoftmaxWarps + (KV8 || VCONV ? kConvWarps : 0));
     }
     for (int i = 0; i < 4 * kHalves; ++i) mbar_init(bar(Lay::B_X + i), 32 * kParts);
+    for (int i = 0; i < kScaleSlotsMax; ++i) mbar_init(bar(Lay::B_SC + i), 1);
     mbar_init(bar(Lay::B_DRAIN), 1);
     prefetch_tmap(&kmap);
     prefetch_tmap(&vmap);
@@ -647,10 +755,23 @@ __global__ void __launch_bounds__(KV8 ? kTileThreads8 : kTileThreads, 1)
         // range, and issues those boxes itself once lane 0 has set the byte count
         const int zk = lane < nbk ? box_z(kt * kKeyTile + lane * box_rows, box_rows) : 0;
         const int zv = VBLK ? (lane < nbv ? box_z(kt * kKeyTile + lane * bs, bs) : 0) : zk;
+        float gks = 1.f, gvs1 = 1.f;  // block scales of 8-key group `lane` (1 past the last key)
+        if constexpr (BSC) {
+          if (lane < kKeyTile / 8) block_scales_of(p, table, kt * kKeyTile + 8 * lane, r.kv_end, r.kvh, gks, gvs1);
+        }
         for (int v = 0; v < 2 && !failed; ++v) {
           const uint32_t slot = g % SLOTS, use = g / SLOTS;
           if (use > 0) wait_warp(bar(Lay::B_EMPTY + slot), (use - 1) & 1u, failed);
           if (failed) break;
+          if constexpr (BSC) {
+            if (v == 0) {
+              const uint32_t fi = (g / 2) % Lay::SCALE_SLOTS;
+              if (lane < kKeyTile / 8)
+                st_scales(base + Lay::SC_OFF + fi * kScaleSlotBytes + 8 * lane, gks, __log2f(gvs1));
+              __syncwarp();
+              if (lane == 0) mbar_arrive(bar(Lay::B_SC + fi));  // release: the range's scales
+            }
+          }
           const void *map = v ? static_cast<const void *>(&vmap) : static_cast<const void *>(&kmap);
           const uint32_t dst = sRing + slot * Lay::KV_BYTES;
           if constexpr (KV8) {
@@ -1059,10 +1180,20 @@ __global__ void __launch_bounds__(KV8 ? kTileThreads8 : kTileThreads, 1)
         // m_used, as separately rounded operations (no contraction into one
         // fused multiply-add): the exponents below are bounded by exactly this
         // difference. The other warp reads its scores before either writes P.
-        const float mx = fmaxf(masked_max32(s0, ck0, lim), masked_max32(s1, ck0 + 32, lim));
+        uint32_t sc = 0;  // block scales: this warp's groups of the range
+        float mx;
+        if constexpr (BSC) {
+          const uint32_t gv = gvs + kt, fi = gv % Lay::SCALE_SLOTS;
+          wait_warp(bar(Lay::B_SC + fi), (gv / Lay::SCALE_SLOTS) & 1u, failed);
+          if (failed) break;
+          sc = base + Lay::SC_OFF + fi * kScaleSlotBytes + part * (PART_KEYS / 8) * 8;
+          mx = fmaxf(scaled_max32(s0, ck0, lim, sl2, sc), scaled_max32(s1, ck0 + 32, lim, sl2, sc + 32));
+        } else {
+          mx = fmaxf(masked_max32(s0, ck0, lim), masked_max32(s1, ck0 + 32, lim));
+        }
         const float mo = exchange(mx);
         if (failed) break;
-        const float cm = __fmul_rn(sl2, fmaxf(mx, mo));
+        const float cm = BSC ? fmaxf(mx, mo) : __fmul_rn(sl2, fmaxf(mx, mo));
         const bool grow = cm > -INFINITY && (m_used == -INFINITY || __fsub_rn(cm, m_used) > kRescaleLog2);
         float alpha = 1.f;  // factor owed by O and l for the growth
         if (grow) {
@@ -1087,7 +1218,22 @@ __global__ void __launch_bounds__(KV8 ? kTileThreads8 : kTileThreads, 1)
         // P of step ks (8 columns at 8 ks) covers only scores read by
         // earlier steps. Rare cases stay out of the loop (inside it, as a
         // branch per step, they cost 2 %).
-        if (vpair) {
+        if constexpr (BSC) {
+          if (exact) {
+            for (int ks = 0; ks < PART_KEYS / 16; ++ks) {
+              uint32_t t[16];
+              tmem_ld16_wait(sp + 16 * ks, t);
+              probs16_scaled_store<true>(t, ck0 + 16 * ks, lim, sl2, ms, sum, sp + 8 * ks, sc + 16 * ks);
+            }
+          } else {
+#pragma unroll 2
+            for (int ks = 0; ks < PART_KEYS / 16; ++ks) {
+              uint32_t t[16];
+              tmem_ld16_wait(sp + 16 * ks, t);
+              probs16_scaled_store<false>(t, ck0 + 16 * ks, lim, sl2, ms, sum, sp + 8 * ks, sc + 16 * ks);
+            }
+          }
+        } else if (vpair) {
           range_probs<true>(sp, ck0, lim, sl2, ms, exact, sum);
         } else if (exact) {
           range_probs<false>(sp, ck0, lim, sl2, ms, true, sum);
@@ -1220,7 +1366,10 @@ struct WideLayout {
   static constexpr int B_FULL = 0, B_EMPTY = kMaxSlots, B_RAW = 2 * kMaxSlots, B_CONV = 3 * kMaxSlots;
   static constexpr int B_S = 4 * kMaxSlots, B_P = B_S + 2, B_O = B_P + 2, B_QF = B_O + 1, B_QE = B_QF + 1;
   static constexpr int B_UF = B_QE + 1, B_UE = B_UF + kUnitSlots, B_X1 = B_UE + kUnitSlots, B_X2 = B_X1 + 4;
-  static constexpr int B_DRAIN = B_X2 + 4, NBARS = B_DRAIN + 1;
+  static constexpr int B_DRAIN = B_X2 + 4, B_SC = B_DRAIN + 1;
+  // Block scales: range g's are written once load 4 g - 5 (V of range g - 2) has been used up.
+  static constexpr int SCALE_SLOTS = 2;
+  static constexpr int NBARS = B_SC + SCALE_SLOTS;
   static constexpr int XCH_BYTES = kWideSoftmaxWarps * 32 * 4;
   static constexpr int REC_BYTES = kUnitSlots * 32;
   static constexpr int FIXED = Q_BYTES + XCH_BYTES + REC_BYTES + 8 * NBARS + 16;
@@ -1232,11 +1381,13 @@ struct WideLayout {
   static constexpr int REC_OFF = XCH_OFF + XCH_BYTES;
   static constexpr int BAR_OFF = REC_OFF + REC_BYTES;
   static constexpr int TMEM_OFF = BAR_OFF + 8 * NBARS;
-  static constexpr int BYTES = TMEM_OFF + 16;
+  static constexpr int SC_OFF = TMEM_OFF + 16;
+  static constexpr int BYTES = SC_OFF + SCALE_SLOTS * kScaleSlotBytes;
 };
+static_assert(WideLayout::SLOTS == 5, "two scale slots");
 static_assert(WideLayout::BYTES <= 227 * 1024, "shared memory of one CTA");
 
-template <int G, typename E, bool KV8>
+template <int G, typename E, bool KV8, bool BSC>
 __global__ void __launch_bounds__(kWideThreads, 1)
     prefill_tile_wide_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap,
                              const TileParams p) {
@@ -1299,6 +1450,7 @@ __global__ void __launch_bounds__(kWideThreads, 1)
       mbar_init(bar(Lay::B_X1 + q), 64);  // the two softmax warps of a lane quadrant
       mbar_init(bar(Lay::B_X2 + q), 64);
     }
+    for (int i = 0; i < Lay::SCALE_SLOTS; ++i) mbar_init(bar(Lay::B_SC + i), 1);
     mbar_init(bar(Lay::B_DRAIN), 1);
     prefetch_tmap(&kmap);
     prefetch_tmap(&vmap);
@@ -1398,10 +1550,23 @@ __global__ void __launch_bounds__(kWideThreads, 1)
       const int nkt = nranges(r);
       for (int kt = 0; kt < nkt && !failed; ++kt) {
         const int z = lane < nbk ? box_z(kt * kKeyTile + lane * box_rows, box_rows) : 0;
+        float gks = 1.f, gvs1 = 1.f;  // block scales of 8-key group `lane` (1 past the last key)
+        if constexpr (BSC) {
+          if (lane < kKeyTile / 8) block_scales_of(p, table, kt * kKeyTile + 8 * lane, r.kv_end, r.kvh, gks, gvs1);
+        }
         for (int v = 0; v < LPR && !failed; ++v) {
           const uint32_t slot = g % SLOTS, use = g / SLOTS;
           if (use > 0) wait_warp(bar(Lay::B_EMPTY + slot), (use - 1) & 1u, failed);
           if (failed) break;
+          if constexpr (BSC) {
+            if (v == 0) {
+              const uint32_t fi = (g / LPR) % Lay::SCALE_SLOTS;
+              if (lane < kKeyTile / 8)
+                st_scales(base + Lay::SC_OFF + fi * kScaleSlotBytes + 8 * lane, gks, __log2f(gvs1));
+              __syncwarp();
+              if (lane == 0) mbar_arrive(bar(Lay::B_SC + fi));  // release: the range's scales
+            }
+          }
           const void *map = v >= 2 ? static_cast<const void *>(&vmap) : static_cast<const void *>(&kmap);
           const int x0 = (v & 1) * 128;  // first element of the unit's half of d
           const uint32_t dst = sRing + slot * Lay::UNIT_BYTES;
@@ -1686,10 +1851,20 @@ __global__ void __launch_bounds__(kWideThreads, 1)
         tc_fence_after();
         uint32_t s0[32], s1[32];
         tmem_ld32x2_wait(sp, s0, s1);
-        const float mx = fmaxf(masked_max32(s0, ck0, lim), masked_max32(s1, ck0 + 32, lim));
+        uint32_t sc = 0;  // block scales: this warp's groups of the range
+        float mx;
+        if constexpr (BSC) {
+          const uint32_t fi = gr % Lay::SCALE_SLOTS;
+          wait_warp(bar(Lay::B_SC + fi), (gr / Lay::SCALE_SLOTS) & 1u, failed);
+          if (failed) break;
+          sc = base + Lay::SC_OFF + fi * kScaleSlotBytes + part * 64;
+          mx = fmaxf(scaled_max32(s0, ck0, lim, sl2, sc), scaled_max32(s1, ck0 + 32, lim, sl2, sc + 32));
+        } else {
+          mx = fmaxf(masked_max32(s0, ck0, lim), masked_max32(s1, ck0 + 32, lim));
+        }
         const float mo = exchange(mx);
         if (failed) break;
-        const float cm = __fmul_rn(sl2, fmaxf(mx, mo));
+        const float cm = BSC ? fmaxf(mx, mo) : __fmul_rn(sl2, fmaxf(mx, mo));
         const bool grow = cm > -INFINITY && (m_used == -INFINITY || __fsub_rn(cm, m_used) > kRescaleLog2);
         float alpha = 1.f;
         if (grow) {
@@ -1699,6 +1874,18 @@ __global__ void __launch_bounds__(kWideThreads, 1)
         const float ms = m_used == -INFINITY ? 0.f : m_used;
         float sum = 0.f;
         constexpr uint32_t PSTEP = SPLIT ? 16 : 8;
+        if constexpr (BSC) {
+          const bool exact = __any_sync(FULL, fabsf(ms) > 4096.f);
+#pragma unroll 1
+          for (int ks = 0; ks < 4; ++ks) {
+            uint32_t t[16];
+            tmem_ld16_wait(sp + 16 * ks, t);
+            if (exact)
+              probs16_scaled_store<true>(t, ck0 + 16 * ks, lim, sl2, ms, sum, sp + 8 * ks, sc + 16 * ks);
+            else
+              probs16_scaled_store<false>(t, ck0 + 16 * ks, lim, sl2, ms, sum, sp + 8 * ks, sc + 16 * ks);
+          }
+        } else {
         if (__any_sync(FULL, fabsf(ms) > 4096.f)) {
           probs16_store<M, true, SPLIT>(s0, ck0, lim, sl2, ms, sum, sp);
           probs16_store<M, true, SPLIT>(s0 + 16, ck0 + 16, lim, sl2, ms, sum, sp + PSTEP);
@@ -1713,6 +1900,7 @@ __global__ void __launch_bounds__(kWideThreads, 1)
         } else {
           probs16_store<M, false, SPLIT>(s1, ck0 + 32, lim, sl2, ms, sum, sp + 2 * PSTEP);
           probs16_store<M, false, SPLIT>(s1 + 16, ck0 + 48, lim, sl2, ms, sum, sp + 3 * PSTEP);
+        }
         }
         // O holds P V(0 .. kt-1) once P V(kt-1) completes (S(kt) may have been
         // issued before it): wait for it only when O must be rescaled
@@ -1792,13 +1980,13 @@ __global__ void __launch_bounds__(kWideThreads, 1)
   if (warp == 0) tmem_dealloc(tmem, kTmemCols);
 }
 
-template <int D, int G, typename E, bool KV8>
+template <int D, int G, typename E, bool KV8, bool BSC>
 cudaError_t launch_prefill_tiles(const CUtensorMap &kmap, const CUtensorMap &vmap, const CUtensorMap &vmapb,
                                  const TileParams &tp, int sm_count, cudaStream_t stream) {
   if constexpr (D == kWideD) {
     (void)vmapb;
     constexpr int smem = WideLayout::BYTES;
-    auto kern = prefill_tile_wide_kernel<G, E, KV8>;
+    auto kern = prefill_tile_wide_kernel<G, E, KV8, BSC>;
     cudaError_t err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (err != cudaSuccess) return err;
     err = cudaFuncSetAttribute(kern, cudaFuncAttributePreferredSharedMemoryCarveout, 100);
@@ -1810,7 +1998,7 @@ cudaError_t launch_prefill_tiles(const CUtensorMap &kmap, const CUtensorMap &vma
     return launch_pdl(kern, dim3(static_cast<unsigned>(grid)), dim3(kWideThreads), smem, stream, kmap, vmap, tp);
   } else {
     constexpr int smem = TcLayout<D>::REQUEST;
-    auto kern = prefill_tile_kernel<D, G, E, KV8>;
+    auto kern = prefill_tile_kernel<D, G, E, KV8, BSC>;
     cudaError_t err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (err != cudaSuccess) return err;
     err = cudaFuncSetAttribute(kern, cudaFuncAttributePreferredSharedMemoryCarveout, 100);
@@ -1824,15 +2012,17 @@ cudaError_t launch_prefill_tiles(const CUtensorMap &kmap, const CUtensorMap &vma
   }
 }
 
-#define PA_TILE_INST1(DD, GG, EE, K8)                                                                   \
-  template cudaError_t launch_prefill_tiles<DD, GG, EE, K8>(const CUtensorMap &, const CUtensorMap &,     \
-                                                            const CUtensorMap &, const TileParams &, int, \
-                                                            cudaStream_t);
+#define PA_TILE_INST1(DD, GG, EE, K8, BS)                                                                  \
+  template cudaError_t launch_prefill_tiles<DD, GG, EE, K8, BS>(const CUtensorMap &, const CUtensorMap &,     \
+                                                                const CUtensorMap &, const TileParams &, int, \
+                                                                cudaStream_t);
 #define PA_TILE_INST(DD, GG)                                                                              \
-  PA_TILE_INST1(DD, GG, ElemBf16, false)                                                                  \
-  PA_TILE_INST1(DD, GG, ElemFp16, false)                                                                  \
-  PA_TILE_INST1(DD, GG, ElemBf16, true)                                                                   \
-  PA_TILE_INST1(DD, GG, ElemFp16, true)
+  PA_TILE_INST1(DD, GG, ElemBf16, false, false)                                                           \
+  PA_TILE_INST1(DD, GG, ElemFp16, false, false)                                                           \
+  PA_TILE_INST1(DD, GG, ElemBf16, true, false)                                                            \
+  PA_TILE_INST1(DD, GG, ElemFp16, true, false)                                                            \
+  PA_TILE_INST1(DD, GG, ElemBf16, true, true)                                                             \
+  PA_TILE_INST1(DD, GG, ElemFp16, true, true)
 PA_TILE_INST(128, 1)
 PA_TILE_INST(128, 2)
 PA_TILE_INST(128, 4)

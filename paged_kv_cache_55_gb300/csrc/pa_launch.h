@@ -41,6 +41,50 @@ cudaError_t launch_gather_kv(const void *key_cache, const void *value_cache, con
                              int32_t seq_len, int32_t row_bytes, int32_t block_size, int64_t num_blocks, void *key_out,
                              void *value_out, unsigned int *status, int sm_count, cudaStream_t stream);
 
+// RMS norm of q and K heads + rotation, into rows or the cache (norm_rope.cu).
+// A null weight pointer skips that norm. Strides in elements.
+struct NormRopeLaunch {
+  const void *q, *key, *value;
+  int64_t q_stride, key_stride, value_stride;
+  const void *q_weight, *k_weight;
+  float eps;
+  void *q_out;
+  int64_t q_out_stride;
+  void *key_dst, *value_dst;  // dst 0: rows of key_out_stride elements (no V); 1, 2: the caches
+  int64_t key_out_stride;
+  const int64_t *slot_mapping, *positions;
+  const float *cos_sin;
+  int64_t num_slots;
+  int32_t max_position, rotary_dim, is_neox;
+  int32_t num_tokens, num_heads, num_kv_heads, head_dim;
+  int32_t dst;  // 0 K rows, 1 16-bit caches, 2 E4M3 caches with one scale each
+  float k_scale, v_scale;
+  int32_t dtype;
+  int32_t slices;  // warps per token (set by the launcher)
+  unsigned int *status;
+};
+cudaError_t launch_norm_rope(const NormRopeLaunch &p, int sm_count, cudaStream_t stream);
+
+// Quantising scatter into 8-bit caches with a scale per (block, KV head) (block_scales.cu).
+struct BlockScatterLaunch {
+  const void *key, *value;
+  int64_t key_stride, value_stride;
+  void *key_cache, *value_cache;
+  float *k_scales, *v_scales;
+  const int32_t *block_tables;
+  int32_t max_blocks_per_seq;
+  const int32_t *seq_lens, *query_start_loc;
+  int32_t num_seqs, total_q, max_query_len;
+  int32_t num_kv_heads, head_dim, block_size;
+  int64_t num_blocks;
+  int32_t dtype;
+  unsigned int *status;
+};
+cudaError_t launch_block_scatter(const BlockScatterLaunch &p, int sm_count, cudaStream_t stream);
+cudaError_t launch_copy_block_scales(float *k_scales, float *v_scales, const int64_t *mapping, int32_t num_pairs,
+                                     int32_t num_kv_heads, int64_t num_blocks, unsigned int *status, int sm_count,
+                                     cudaStream_t stream);
+
 // Byte offsets of the pieces of the attention workspace, and the split plan.
 struct WorkspaceLayout {
   size_t item_start, nparts, item_count, items, tiles, part_lse, part_o, total;
@@ -70,6 +114,7 @@ struct AttnLaunch {
   int32_t dtype;  // PA_BF16 or PA_FP16 (q and out; the caches too unless kv_fp8)
   bool kv_fp8;    // caches hold E4M3 codes: K = code * k_scale, V = code * v_scale
   float k_scale, v_scale;
+  const float *k_scales, *v_scales;  // [num_blocks][num_kv_heads], or null: one scale per cache
   void *out;
   void *workspace;
   unsigned int *status;
