@@ -99,6 +99,19 @@ def load_library(path: str = LIBRARY) -> ctypes.CDLL:
     return lib
 
 
+_NATIVE = None
+
+
+def _native():
+    """The native marshalling module (built beside the library, linked to it)."""
+    global _NATIVE
+    if _NATIVE is None:
+        _lib()  # names the build command if nothing has been built
+        from . import _native as module
+        _NATIVE = module
+    return _NATIVE
+
+
 def _lib() -> ctypes.CDLL:
     global _LIB
     if _LIB is None:
@@ -235,33 +248,6 @@ def _index_tensors(*named) -> None:
 def _workspace(workspace: torch.Tensor) -> None:
     if not isinstance(workspace, torch.Tensor) or not workspace.is_cuda or not workspace.is_contiguous():
         raise TypeError("workspace must be a contiguous CUDA tensor")
-
-
-def _here(*named) -> None:
-    """Every tensor on the current CUDA device, whose stream the call uses."""
-    device = torch.cuda.current_device()
-    for t, n in named:
-        if t.device.index != device:
-            raise ValueError(f"{n} is on {t.device}; the current device is cuda:{device}")
-
-
-def _head_rows(t: torch.Tensor, name: str) -> None:
-    if t.stride(2) != 1 or (t.stride(1) != t.shape[2] and t.shape[1] != 1):
-        raise ValueError(f"each token row of {name} must be [heads, D] contiguous")
-
-
-def _contiguous(*named) -> None:
-    for t, n in named:
-        if not t.is_contiguous():
-            raise ValueError(f"{n} must be contiguous")
-
-
-def _block_scale_shapes(k_scales: torch.Tensor, v_scales: torch.Tensor, num_blocks: int, num_kv_heads: int) -> None:
-    """k_scales and v_scales float32 [num_blocks, num_kv_heads]."""
-    for t, n in ((k_scales, "k_scales"), (v_scales, "v_scales")):
-        _need(t, n, torch.float32)
-        if tuple(t.shape) != (num_blocks, num_kv_heads):
-            raise ValueError(f"{n} {tuple(t.shape)} must be [num_blocks, num_kv_heads] ({num_blocks}, {num_kv_heads})")
 
 
 def pa_reshape_and_cache(key: torch.Tensor, value: torch.Tensor, key_cache: torch.Tensor,
@@ -455,32 +441,18 @@ def pa_rope_reshape_and_cache_fp8(q: torch.Tensor, key: torch.Tensor, value: tor
            "pa_rope_reshape_and_cache_fp8")
 
 
-def _norm_rope_args(q, key, q_weight, k_weight, eps, positions, cos_sin_cache, q_out, others):
-    """Checks shared by the norm_rope calls; returns (dtype, weight pointers)."""
-    named = [(q, "q"), (key, "key"), (q_out, "q_out"), *others]
-    named += [(w, n) for w, n in ((q_weight, "q_weight"), (k_weight, "k_weight")) if w is not None]
-    dt = _elem_code(*named)
-    _need(positions, "positions", torch.int64)
-    _need(cos_sin_cache, "cos_sin_cache", torch.float32)
-    _here(*named, (positions, "positions"), (cos_sin_cache, "cos_sin_cache"))
-    _dims(q, 3, "q")
-    _dims(key, 3, "key")
-    if q.shape[0] != key.shape[0] or q.shape[2] != key.shape[2]:
-        raise ValueError(f"q {tuple(q.shape)} must be [T, H, D] for key {tuple(key.shape)}")
-    if q_out.shape != q.shape:
-        raise ValueError(f"q_out {tuple(q_out.shape)} must have q's shape {tuple(q.shape)}")
-    for w, n in ((q_weight, "q_weight"), (k_weight, "k_weight")):
-        if w is not None and (tuple(w.shape) != (q.shape[2],) or not w.is_contiguous()):
-            raise ValueError(f"{n} must be contiguous [{q.shape[2]}], got {tuple(w.shape)}")
-    _dims(positions, 1, "positions")
-    if positions.shape[0] != q.shape[0]:
-        raise ValueError(f"positions has {positions.shape[0]} entries for {q.shape[0]} tokens")
-    _dims(cos_sin_cache, 2, "cos_sin_cache")
-    _contiguous((positions, "positions"), (cos_sin_cache, "cos_sin_cache"))
-    for t, n in ((q, "q"), (key, "key"), (q_out, "q_out")):
-        _head_rows(t, n)
-    return dt, None if q_weight is None else q_weight.data_ptr(), None if k_weight is None else k_weight.data_ptr()
+def _check_native(status: int, what: str) -> None:
+    if status:
+        _check(status, what)
 
+
+def _stream_or_current(stream):
+    """None (the native module reads the current stream) or a stream handle."""
+    return None if stream is None else _stream(stream)
+
+
+# The calls below marshal their arguments in the native module: same checks and
+# errors, a tenth of the time. Tensors must be on the current CUDA device.
 
 def pa_norm_rope(q: torch.Tensor, key: torch.Tensor, q_weight: Optional[torch.Tensor],
                  k_weight: Optional[torch.Tensor], eps: float, positions: torch.Tensor, cos_sin_cache: torch.Tensor,
@@ -488,17 +460,8 @@ def pa_norm_rope(q: torch.Tensor, key: torch.Tensor, q_weight: Optional[torch.Te
     """RMS norm of every head of q [T, H, D] and key [T, Hkv, D] (weights [D]; None: no norm), then
     the rotation, into q_out and key_out (q and key themselves, or other rows; token strides free).
     positions int64 [T]; cos_sin_cache float32 [max_position, rotary_dim]."""
-    dt, qw, kw = _norm_rope_args(q, key, q_weight, k_weight, eps, positions, cos_sin_cache, q_out,
-                                 [(key_out, "key_out")])
-    if key_out.shape != key.shape:
-        raise ValueError(f"key_out {tuple(key_out.shape)} must have key's shape {tuple(key.shape)}")
-    _head_rows(key_out, "key_out")
-    T, H, D = q.shape
-    max_pos, rot = cos_sin_cache.shape
-    _check(_lib().pa_norm_rope(q.data_ptr(), q.stride(0), key.data_ptr(), key.stride(0), qw, kw, float(eps),
-                               positions.data_ptr(), cos_sin_cache.data_ptr(), max_pos, rot, int(bool(is_neox)), T, H,
-                               key.shape[1], D, q_out.data_ptr(), q_out.stride(0), key_out.data_ptr(),
-                               key_out.stride(0), dt, _stream(stream)), "pa_norm_rope")
+    _check_native(_native().norm_rope(q, key, q_weight, k_weight, eps, positions, cos_sin_cache, q_out, key_out,
+                                      is_neox, _stream_or_current(stream)), "pa_norm_rope")
 
 
 def pa_norm_rope_reshape_and_cache(q: torch.Tensor, key: torch.Tensor, value: torch.Tensor,
@@ -508,21 +471,9 @@ def pa_norm_rope_reshape_and_cache(q: torch.Tensor, key: torch.Tensor, value: to
                                    is_neox: bool = True, stream=None) -> None:
     """pa_norm_rope with key's rows and value [T, Hkv, D] written into the caches
     [NB, bs, Hkv, D] (q's type) at slot_mapping int64 [T]; negative slots are padding."""
-    dt, qw, kw = _norm_rope_args(q, key, q_weight, k_weight, eps, positions, cos_sin_cache, q_out,
-                                 [(value, "value"), (key_cache, "key_cache"), (value_cache, "value_cache")])
-    _need(slot_mapping, "slot_mapping", torch.int64)
-    _here((slot_mapping, "slot_mapping"))
-    _scatter_shapes(key, value, key_cache, value_cache, slot_mapping)
-    _head_rows(value, "value")
-    _contiguous((key_cache, "key_cache"), (value_cache, "value_cache"), (slot_mapping, "slot_mapping"))
-    T, H, D = q.shape
-    nb, bs = key_cache.shape[0], key_cache.shape[1]
-    max_pos, rot = cos_sin_cache.shape
-    _check(_lib().pa_norm_rope_reshape_and_cache(
-        q.data_ptr(), q.stride(0), key.data_ptr(), value.data_ptr(), key.stride(0), value.stride(0), qw, kw,
-        float(eps), key_cache.data_ptr(), value_cache.data_ptr(), slot_mapping.data_ptr(), positions.data_ptr(),
-        cos_sin_cache.data_ptr(), max_pos, rot, int(bool(is_neox)), T, H, key.shape[1], D, bs, nb, q_out.data_ptr(),
-        q_out.stride(0), dt, _stream(stream)), "pa_norm_rope_reshape_and_cache")
+    _check_native(_native().norm_rope_cache(q, key, value, q_weight, k_weight, eps, key_cache, value_cache,
+                                            slot_mapping, positions, cos_sin_cache, None, None, q_out, is_neox,
+                                            _stream_or_current(stream)), "pa_norm_rope_reshape_and_cache")
 
 
 def pa_norm_rope_reshape_and_cache_fp8(q: torch.Tensor, key: torch.Tensor, value: torch.Tensor,
@@ -533,37 +484,10 @@ def pa_norm_rope_reshape_and_cache_fp8(q: torch.Tensor, key: torch.Tensor, value
                                        q_out: torch.Tensor, is_neox: bool = True, stream=None) -> None:
     """pa_norm_rope_reshape_and_cache into 8-bit caches (uint8 [NB, bs, Hkv, D] of E4M3 codes of
     x / k_scale and x / v_scale)."""
-    dt, qw, kw = _norm_rope_args(q, key, q_weight, k_weight, eps, positions, cos_sin_cache, q_out,
-                                 [(value, "value")])
-    _need(key_cache, "key_cache", torch.uint8)
-    _need(value_cache, "value_cache", torch.uint8)
-    _need(slot_mapping, "slot_mapping", torch.int64)
-    _here((key_cache, "key_cache"), (value_cache, "value_cache"), (slot_mapping, "slot_mapping"))
-    _scatter_shapes(key, value, key_cache, value_cache, slot_mapping)
-    _head_rows(value, "value")
-    _contiguous((key_cache, "key_cache"), (value_cache, "value_cache"), (slot_mapping, "slot_mapping"))
-    T, H, D = q.shape
-    nb, bs = key_cache.shape[0], key_cache.shape[1]
-    max_pos, rot = cos_sin_cache.shape
-    _check(_lib().pa_norm_rope_reshape_and_cache_fp8(
-        q.data_ptr(), q.stride(0), key.data_ptr(), value.data_ptr(), key.stride(0), value.stride(0), qw, kw,
-        float(eps), key_cache.data_ptr(), value_cache.data_ptr(), slot_mapping.data_ptr(), positions.data_ptr(),
-        cos_sin_cache.data_ptr(), max_pos, rot, int(bool(is_neox)), T, H, key.shape[1], D, bs, nb, float(k_scale),
-        float(v_scale), q_out.data_ptr(), q_out.stride(0), dt, _stream(stream)),
-        "pa_norm_rope_reshape_and_cache_fp8")
-
-
-def _step_shapes(num_tokens: int, block_tables: torch.Tensor, seq_lens: torch.Tensor,
-                 query_start_loc: torch.Tensor) -> int:
-    """block_tables [B, M], seq_lens [B], query_start_loc [B+1]; returns B."""
-    _dims(seq_lens, 1, "seq_lens")
-    _dims(block_tables, 2, "block_tables")
-    _dims(query_start_loc, 1, "query_start_loc")
-    b = seq_lens.shape[0]
-    if block_tables.shape[0] != b or query_start_loc.shape[0] != b + 1:
-        raise ValueError(f"{b} requests need block_tables [{b}, M] and query_start_loc [{b + 1}], got "
-                         f"{tuple(block_tables.shape)} and {tuple(query_start_loc.shape)}")
-    return b
+    _check_native(_native().norm_rope_cache(q, key, value, q_weight, k_weight, eps, key_cache, value_cache,
+                                            slot_mapping, positions, cos_sin_cache, float(k_scale), float(v_scale),
+                                            q_out, is_neox, _stream_or_current(stream)),
+                  "pa_norm_rope_reshape_and_cache_fp8")
 
 
 def pa_reshape_and_cache_fp8_block(key: torch.Tensor, value: torch.Tensor, key_cache: torch.Tensor,
@@ -574,32 +498,9 @@ def pa_reshape_and_cache_fp8_block(key: torch.Tensor, value: torch.Tensor, key_c
     stride free) are the requests' last rows (query_start_loc int32 [B+1], seq_lens int32 [B],
     block_tables int32 [B, M]); caches uint8 [NB, bs, Hkv, D]; k_scales and v_scales float32
     [NB, Hkv], updated: a power of two under which a block's largest magnitude is at most 448."""
-    dt = _elem_code((key, "key"), (value, "value"))
-    _need(key_cache, "key_cache", torch.uint8)
-    _need(value_cache, "value_cache", torch.uint8)
-    _dims(key, 3, "key")
-    if value.shape != key.shape:
-        raise ValueError(f"value {tuple(value.shape)} must have key's shape {tuple(key.shape)}")
-    _cache_pair_shapes(key_cache, value_cache)
-    if tuple(key_cache.shape[2:]) != tuple(key.shape[1:]):
-        raise ValueError(f"cache rows {tuple(key_cache.shape[2:])} must be key's [Hkv, D] {tuple(key.shape[1:])}")
-    T, hkv, d = key.shape
-    nb, bs = key_cache.shape[0], key_cache.shape[1]
-    _block_scale_shapes(k_scales, v_scales, nb, hkv)
-    _index_tensors((block_tables, "block_tables"), (seq_lens, "seq_lens"), (query_start_loc, "query_start_loc"))
-    b = _step_shapes(T, block_tables, seq_lens, query_start_loc)
-    _here((key, "key"), (value, "value"), (key_cache, "key_cache"), (value_cache, "value_cache"),
-          (k_scales, "k_scales"), (v_scales, "v_scales"), (block_tables, "block_tables"), (seq_lens, "seq_lens"),
-          (query_start_loc, "query_start_loc"))
-    _head_rows(key, "key")
-    _head_rows(value, "value")
-    _contiguous((key_cache, "key_cache"), (value_cache, "value_cache"), (k_scales, "k_scales"),
-                (v_scales, "v_scales"))
-    _check(_lib().pa_reshape_and_cache_fp8_block(
-        key.data_ptr(), value.data_ptr(), key.stride(0), value.stride(0), key_cache.data_ptr(),
-        value_cache.data_ptr(), k_scales.data_ptr(), v_scales.data_ptr(), block_tables.data_ptr(),
-        block_tables.shape[1], seq_lens.data_ptr(), query_start_loc.data_ptr(), b, T, max_query_len, hkv, d, bs, nb,
-        dt, _stream(stream)), "pa_reshape_and_cache_fp8_block")
+    _check_native(_native().block_scatter(key, value, key_cache, value_cache, k_scales, v_scales, block_tables,
+                                          seq_lens, query_start_loc, max_query_len, _stream_or_current(stream)),
+                  "pa_reshape_and_cache_fp8_block")
 
 
 def pa_attention_varlen_fp8_block(q: torch.Tensor, key_cache: torch.Tensor, value_cache: torch.Tensor,
@@ -609,43 +510,17 @@ def pa_attention_varlen_fp8_block(q: torch.Tensor, key_cache: torch.Tensor, valu
                                   stream=None) -> None:
     """pa_attention_varlen_fp8 with block scales: the values of block n and KV head h are
     code * k_scales[n, h] and code * v_scales[n, h] (float32 [NB, Hkv], positive)."""
-    dt = _elem_code((q, "q"), (out, "out"))
-    _need(key_cache, "key_cache", torch.uint8)
-    _need(value_cache, "value_cache", torch.uint8)
-    _index_tensors((block_tables, "block_tables"), (seq_lens, "seq_lens"), (query_start_loc, "query_start_loc"))
-    _attention_shapes(q, key_cache, value_cache, block_tables, seq_lens, query_start_loc, out)
-    _workspace(workspace)
-    nb, bs, hkv, _ = key_cache.shape
-    _block_scale_shapes(k_scales, v_scales, nb, hkv)
-    _here((q, "q"), (out, "out"), (key_cache, "key_cache"), (value_cache, "value_cache"), (k_scales, "k_scales"),
-          (v_scales, "v_scales"), (block_tables, "block_tables"), (seq_lens, "seq_lens"),
-          (query_start_loc, "query_start_loc"), (workspace, "workspace"))
-    _contiguous((out, "out"), (key_cache, "key_cache"), (value_cache, "value_cache"), (k_scales, "k_scales"),
-                (v_scales, "v_scales"))
-    _head_rows(q, "q")
-    T, H, D = q.shape
-    _check(_lib().pa_attention_varlen_fp8_block(
-        q.data_ptr(), q.stride(0), key_cache.data_ptr(), value_cache.data_ptr(), k_scales.data_ptr(),
-        v_scales.data_ptr(), block_tables.data_ptr(), block_tables.shape[1], seq_lens.data_ptr(),
-        query_start_loc.data_ptr(), seq_lens.shape[0], T, max_query_len, max_seq_len, H, hkv, D, bs, nb, float(scale),
-        out.data_ptr(), workspace.data_ptr(), workspace.numel() * workspace.element_size(), dt, _stream(stream)),
-        "pa_attention_varlen_fp8_block")
+    _check_native(_native().block_attention(q, key_cache, value_cache, k_scales, v_scales, block_tables, seq_lens,
+                                            query_start_loc, max_query_len, max_seq_len, scale, out, workspace,
+                                            _stream_or_current(stream)), "pa_attention_varlen_fp8_block")
 
 
 def pa_copy_block_scales(k_scales: torch.Tensor, v_scales: torch.Tensor, block_mapping: torch.Tensor,
                          stream=None) -> None:
     """The scales' part of a copy-on-write copy: rows block_mapping[:, 1] of k_scales and v_scales
     (float32 [NB, Hkv]) become rows block_mapping[:, 0] (int64 [n, 2] on the device)."""
-    _dims(k_scales, 2, "k_scales")
-    nb, hkv = k_scales.shape
-    _block_scale_shapes(k_scales, v_scales, nb, hkv)
-    _need(block_mapping, "block_mapping", torch.int64)
-    if block_mapping.dim() != 2 or block_mapping.shape[1] != 2:
-        raise ValueError("block_mapping must be [n, 2]")
-    _here((k_scales, "k_scales"), (v_scales, "v_scales"), (block_mapping, "block_mapping"))
-    _contiguous((k_scales, "k_scales"), (v_scales, "v_scales"), (block_mapping, "block_mapping"))
-    _check(_lib().pa_copy_block_scales(k_scales.data_ptr(), v_scales.data_ptr(), block_mapping.data_ptr(),
-                                       block_mapping.shape[0], hkv, nb, _stream(stream)), "pa_copy_block_scales")
+    _check_native(_native().copy_block_scales(k_scales, v_scales, block_mapping, _stream_or_current(stream)),
+                  "pa_copy_block_scales")
 
 
 def pa_copy_blocks(key_cache: torch.Tensor, value_cache: torch.Tensor, block_mapping: torch.Tensor,
