@@ -146,7 +146,7 @@ pa_status pa_reshape_and_cache_fp8(const void *key, const void *value,
                                    float k_scale, float v_scale, int32_t dtype, void *stream);
 
 /*
- * Bytes of device workspace pa_attention_varlen or pa_attention_varlen_fp8 needs for these host-side
+ * Bytes of device workspace pa_attention_varlen and its 8-bit forms need for these host-side
  * bounds (0 if the arguments are invalid). Pure host arithmetic; no CUDA call.
  * The workspace holds the work plan and the split-KV partial results.
  */

@@ -179,12 +179,15 @@ size_t pa_attention_workspace_size(int32_t num_seqs, int32_t total_q_tokens, int
                                    int32_t head_dim, int32_t block_size) {
   if (max_query_len < 0 || max_seq_len < max_query_len) return 0;
   if (!supported_dims(num_heads, num_kv_heads, head_dim, block_size)) return 0;
-  // one size for either cache type: the larger of the two plans
+  // one size for every cache type: the largest of the plans
   pa::WorkspaceLayout w16, w8;
+  pa::BlockWorkspace wb;
   if (!pa::workspace_layout(num_seqs, total_q_tokens, max_seq_len, num_heads, num_kv_heads, head_dim, false, w16) ||
-      !pa::workspace_layout(num_seqs, total_q_tokens, max_seq_len, num_heads, num_kv_heads, head_dim, true, w8))
+      !pa::workspace_layout(num_seqs, total_q_tokens, max_seq_len, num_heads, num_kv_heads, head_dim, true, w8) ||
+      !pa::block_workspace_layout(num_seqs, total_q_tokens, max_seq_len, num_heads, num_kv_heads, head_dim, wb))
     return 0;
-  return w16.total > w8.total ? w16.total : w8.total;
+  const size_t w = w16.total > w8.total ? w16.total : w8.total;
+  return w > wb.total ? w : wb.total;
 }
 
 pa_status pa_attention_plan_info(int32_t num_seqs, int32_t max_seq_len, int32_t num_heads,
@@ -232,10 +235,19 @@ pa_status attention_call(const void *q, int64_t q_token_stride, const void *key_
   if (!aligned(key_cache, 16) || !aligned(value_cache, 16) || !aligned(out, 16) || !aligned(block_tables, 4) ||
       !aligned(seq_lens, 4) || !aligned(query_start_loc, 4))
     return PA_ERR_ALIGN;
-  pa::WorkspaceLayout w;
-  if (!pa::workspace_layout(num_seqs, total_q_tokens, max_seq_len, num_heads, num_kv_heads, head_dim, kv_fp8, w))
-    return PA_ERR_DIMS;
-  if (!workspace || workspace_bytes < w.total) return PA_ERR_WORKSPACE;
+  size_t need = 0;
+  if (k_scales) {
+    pa::BlockWorkspace w;
+    if (!pa::block_workspace_layout(num_seqs, total_q_tokens, max_seq_len, num_heads, num_kv_heads, head_dim, w))
+      return PA_ERR_DIMS;
+    need = w.total;
+  } else {
+    pa::WorkspaceLayout w;
+    if (!pa::workspace_layout(num_seqs, total_q_tokens, max_seq_len, num_heads, num_kv_heads, head_dim, kv_fp8, w))
+      return PA_ERR_DIMS;
+    need = w.total;
+  }
+  if (!workspace || workspace_bytes < need) return PA_ERR_WORKSPACE;
   if (!aligned(workspace, 256)) return PA_ERR_ALIGN;
   DeviceState *ds = device_state();
   if (!ds) return PA_ERR_CUDA;
@@ -274,7 +286,8 @@ pa_status attention_call(const void *q, int64_t q_token_stride, const void *key_
   a.tile_start = tile_start;
   a.tile_stop = tile_stop;
   int launched = 0;
-  cudaError_t err = pa::launch_attention(a, static_cast<cudaStream_t>(stream), &launched);
+  const auto launch = k_scales ? pa::launch_block_attention : pa::launch_attention;
+  cudaError_t err = launch(a, static_cast<cudaStream_t>(stream), &launched);
   g_launches.fetch_add(static_cast<uint64_t>(launched));
   if (err != cudaSuccess) return cuda_failure(PA_ERR_LAUNCH, err);
   return PA_OK;

@@ -1,0 +1,1036 @@
+// Attention over 8-bit caches with a scale per (block, KV head): planning,
+// split-KV decode and the log-sum-exp merge. Chunked-prefill requests go to
+// the tensor-core tiles of attention_prefill_tc.cu.
+//
+// The mathematics. With x_j = scale q.Kc_j ks_j log2 e + log2 vs_j (ks_j, vs_j
+// the scales of key j's block) and any reference m,
+//   P'_j = 2^(x_j - m),  O = sum_j P'_j Vc_j,  l = sum_j P'_j / vs_j,  out = O / l,
+// since P'_j / vs_j = 2^(scale q.K_j log2 e - m) is the plain softmax weight.
+// Folding vs into the exponent keeps P' within the fp16 operand's range
+// whatever the scales are, with one maximum and one exponent per score.
+//
+// The decode kernel is bound by HBM: a key costs 2 D bytes per KV head. Its
+// work units are (request, KV head, run of 32-key tiles); a unit's 8 columns
+// are the (query row, head of the GQA group) pairs, so each byte is read once.
+// Every warp is an independent pipeline (own TMA ring, no CTA barrier), takes
+// units from a queue, and computes S^T[16 keys x 8 columns] = K Q^T and
+// O^T += V^T P^T with m16n8k16 fp16 products, codes widened exactly in
+// registers. What it does per tile was cut to what the 32 keys need:
+//   * the reference m is only moved when a score exceeds it by 2^8 (a warp
+//     vote; P' then stays below 2^8 <= fp16's range), so most tiles reduce no
+//     maximum and rescale nothing;
+//   * one fp16 P' per key (11 bits: a weight moves by at most 2^-11 of itself);
+//   * masks only in a unit's last tiles; K's four codes of a word are used in
+//     the order the widening leaves them (q is loaded to match);
+//   * block-table entries are loaded one tile ahead, the boxes of a tile are
+//     issued by as many lanes, and its scales travel with it by cp.async on
+//     the same mbarrier.
+// The planner sizes units from the step's actual lengths, so that a single
+// short request still spreads over the GPU and long ones end together.
+#include <cuda.h>
+#include <cudaTypedefs.h>
+#include <float.h>
+
+#include <mutex>
+#include <type_traits>
+
+#include "attention_internal.cuh"
+#include "pa_launch.h"
+
+namespace pa {
+
+namespace {
+
+constexpr int kCols = 8;    // (query row, head) columns per unit
+constexpr int kTile = 32;   // keys per ring tile
+constexpr int kRingBytes = 192 * 1024;
+constexpr uint64_t kWaitNs = 2000000000;  // 2 s: a TMA never takes this long
+constexpr float kGrowLog2 = 8.f;          // P' <= 2^8 between moves of the reference
+
+// Decode warps per SM: a slot (K and V of one tile) is 2 x 32 rows of 64, 128
+// or 256 codes; at head_dim 256 six warps of two slots fill the ring.
+constexpr int block_warps(int head_dim) { return head_dim == 256 ? 6 : 12; }
+// Warps of the whole GPU that units are sized for. A fixed figure (152 SMs),
+// so that the sizing calls need no device query.
+constexpr int64_t unit_warps(int head_dim) { return 152 * block_warps(head_dim); }
+
+// Unit size in tiles for `total` tiles (over all KV heads): one unit per warp
+// while that is at most kMinUnit tiles, else up to kUnitsPerWarp units per
+// warp of at least kMinUnit tiles (the queue then evens out requests of
+// different lengths).
+constexpr int kUnitsPerWarp = 3, kMinUnit = 8;
+__host__ __device__ inline int64_t unit_tiles(int64_t total, int64_t warps) {
+  const int64_t one = (total + warps - 1) / warps;
+  int64_t u = (one + kUnitsPerWarp - 1) / kUnitsPerWarp;
+  const int64_t low = one < kMinUnit ? one : kMinUnit;
+  u = u < low ? low : u;
+  return u < 1 ? 1 : u;
+}
+
+struct PlanParams {
+  const int32_t *seq_lens, *query_start_loc;
+  int32_t num_seqs, total_q, max_query_len, max_seq_len, max_blocks_per_seq, block_size;
+  int32_t num_kv_heads;
+  int32_t rows_per_item;  // 8 / G
+  int32_t tile_pos;       // query positions per prefill tile
+  int32_t max_items, max_tiles;
+  int64_t warps;          // unit_warps
+  int32_t first_units;    // units the decode warps take without the queue
+  int32_t *nparts, *first_full, *rest;  // per request: partitions, item of the first full one, of the partial last (or -1)
+  int32_t *counts;                      // items, queue, prefill tiles, their queue
+  int4 *items, *tiles;
+  unsigned int *status;
+};
+
+struct DecodeParams {
+  const bf16 *q;
+  int64_t q_stride;
+  const int32_t *block_tables;
+  int32_t max_blocks_per_seq, block_size, block_shift;
+  int32_t num_heads, num_kv_heads;
+  int64_t num_blocks;
+  const float *k_scales, *v_scales;
+  float scale_log2;
+  bf16 *out;
+  const int4 *items;
+  int32_t *counts;
+  int32_t num_seqs, total_q, max_items;
+  float *part_o;    // [max_items][Hkv][8][D]
+  float *part_lse;  // [max_items][Hkv][8]
+  int32_t tiles_follow;
+  unsigned int *status;
+};
+
+struct MergeParams {
+  const int32_t *query_start_loc, *nparts, *first_full, *rest;
+  int32_t num_kv_heads, num_heads, max_items;
+  const float *part_o, *part_lse;
+  bf16 *out;
+};
+
+// ---- planning --------------------------------------------------------------
+
+// Exclusive scan over a block of NT threads (at most 1024); *total: the sum.
+template <int NT>
+__device__ __forceinline__ unsigned long long block_scan(unsigned long long v, unsigned long long *warp_tot,
+                                                         unsigned long long *total) {
+  constexpr int NWARP = NT / 32;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  unsigned long long incl = v;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const unsigned long long t = __shfl_up_sync(0xffffffffu, incl, o);
+    if (lane >= o) incl += t;
+  }
+  __syncthreads();  // warp_tot of the previous scan has been read
+  if (lane == 31) warp_tot[warp] = incl;
+  __syncthreads();
+  if (warp == 0) {
+    unsigned long long t = lane < NWARP ? warp_tot[lane] : 0;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const unsigned long long u = __shfl_up_sync(0xffffffffu, t, o);
+      if (lane >= o) t += u;
+    }
+    if (lane < NWARP) warp_tot[lane] = t;
+  }
+  __syncthreads();
+  *total = warp_tot[NWARP - 1];
+  return (warp > 0 ? warp_tot[warp - 1] : 0) + incl - v;
+}
+
+struct Request {
+  int q0, ql, len;
+  int key_tiles;  // 32-key tiles of a decode request (0: none)
+  int tiles;      // prefill tiles of a longer one
+};
+
+__device__ __forceinline__ Request read_request(const PlanParams &p, int b, bool report) {
+  Request r;
+  r.q0 = ld_cg(p.query_start_loc + b);
+  const int q1 = ld_cg(p.query_start_loc + b + 1);
+  r.len = ld_cg(p.seq_lens + b);
+  r.ql = q1 - r.q0;
+  r.key_tiles = r.tiles = 0;
+  if (r.q0 < 0 || r.ql < 0 || q1 > p.total_q || (b == 0 && r.q0 != 0)) {
+    if (report) flag_error(p.status, PA_FLAG_QUERY_LOC);
+    return r;
+  }
+  if (report && b == p.num_seqs - 1 && q1 != p.total_q) flag_error(p.status, PA_FLAG_QUERY_LOC);
+  if (r.len < r.ql || r.len > p.max_seq_len || r.ql > p.max_query_len ||
+      r.len > static_cast<int64_t>(p.max_blocks_per_seq) * p.block_size) {
+    if (report) flag_error(p.status, PA_FLAG_LENGTHS);
+    return r;
+  }
+  if (r.ql == 0) return r;
+  if (r.ql > p.rows_per_item)
+    r.tiles = (r.ql + p.tile_pos - 1) / p.tile_pos;
+  else
+    r.key_tiles = (r.len - 1) / kTile + 1;
+  return r;
+}
+
+// Index r of the half-open prefix range [pre[r], pre[r + 1]) that holds i (n ranges).
+__device__ __forceinline__ int find_range(const int *pre, int n, int i) {
+  int lo = 0;
+  while (n > 1) {
+    const int half = n >> 1;
+    if (pre[lo + half] <= i) {
+      lo += half;
+      n -= half;
+    } else {
+      n = half;
+    }
+  }
+  return lo;
+}
+
+// One CTA. Three sweeps over the requests (the lengths stay in registers when
+// NT threads cover them): the tiles of all decode requests, hence the unit
+// size U; the number of full units, whose items come first in the queue; then
+// the items, each request's key_tiles / U full ones and one of the remainder,
+// written by all threads (a thread finds an item's request in the prefix sums).
+// Item: {b, first query row, rows, position of the first}, {key begin, key
+// end, partition (-1: the whole range), partitions}.
+template <int NT>
+__global__ void __launch_bounds__(NT) block_plan_kernel(const PlanParams p) {
+  __shared__ unsigned long long warp_tot[32];
+  __shared__ int pre_full[NT + 1], pre_tile[NT + 1], s_q0[NT], s_ql[NT], s_len[NT];
+  const int tid = threadIdx.x;
+  griddep_wait();
+  griddep_launch_dependents();
+  const bool once = p.num_seqs <= NT;
+  Request r{};
+  unsigned long long mine = 0, total;
+  for (int b = tid; b < p.num_seqs; b += NT) {
+    r = read_request(p, b, true);
+    mine += r.key_tiles;
+  }
+  block_scan<NT>(mine, warp_tot, &total);
+  const int64_t U64 = unit_tiles(static_cast<int64_t>(total) * p.num_kv_heads, p.warps);
+  const int U = U64 > (1 << 24) ? (1 << 24) : static_cast<int>(U64);
+  const int unit_keys = U * kTile;
+  mine = 0;
+  for (int b = tid; b < p.num_seqs; b += NT) {
+    if (!once) r = read_request(p, b, false);
+    mine += r.key_tiles / U;
+  }
+  unsigned long long full_total;
+  block_scan<NT>(mine, warp_tot, &full_total);
+  const int all_full = static_cast<int>(min(full_total, static_cast<unsigned long long>(p.max_items)));
+  int carry_full = 0, carry_rest = 0, carry_tile = 0;
+  for (int base = 0; base < p.num_seqs; base += NT) {
+    const int b = base + tid, n = min(NT, p.num_seqs - base);
+    if (!once) {
+      r = Request{};
+      if (b < p.num_seqs) r = read_request(p, b, false);
+    }
+    if (b >= p.num_seqs) r = Request{};
+    const int full = r.key_tiles / U, rest = r.key_tiles % U ? 1 : 0;
+    unsigned long long tot, tile_tot;
+    const unsigned long long ex =
+        block_scan<NT>(static_cast<unsigned long long>(full) | (static_cast<unsigned long long>(rest) << 40), warp_tot,
+                       &tot);
+    const unsigned long long ex_tile = block_scan<NT>(static_cast<unsigned long long>(r.tiles), warp_tot, &tile_tot);
+    const int ex_full = static_cast<int>(ex & ((1ull << 40) - 1)), n_full = static_cast<int>(tot & ((1ull << 40) - 1));
+    const int n_tile = static_cast<int>(tile_tot);
+    pre_full[tid] = ex_full;
+    pre_tile[tid] = static_cast<int>(ex_tile);
+    s_q0[tid] = r.q0;
+    s_ql[tid] = r.ql;
+    s_len[tid] = r.len;
+    if (b < p.num_seqs) {
+      const int item = all_full + carry_rest + static_cast<int>(ex >> 40);
+      p.nparts[b] = full + rest;
+      p.first_full[b] = carry_full + ex_full;
+      p.rest[b] = rest ? item : -1;
+      if (rest && item < p.max_items) {
+        p.items[2 * item] = make_int4(b, r.q0, r.ql, r.len - r.ql);
+        p.items[2 * item + 1] = make_int4(full * unit_keys, r.len, full ? full : -1, full + rest);
+      }
+    }
+    __syncthreads();
+    for (int i = tid; i < n_full; i += NT) {
+      const int item = carry_full + i;
+      if (item >= p.max_items) break;
+      const int k = find_range(pre_full, n, i), part = i - pre_full[k];
+      const int len = s_len[k], np = ((len - 1) / kTile + U) / U;
+      p.items[2 * item] = make_int4(base + k, s_q0[k], s_ql[k], len - s_ql[k]);
+      p.items[2 * item + 1] =
+          make_int4(part * unit_keys, static_cast<int>(min(static_cast<long long>(len), (part + 1LL) * unit_keys)),
+                    np > 1 ? part : -1, np);
+    }
+    for (int i = tid; i < n_tile; i += NT) {
+      const int tile = carry_tile + i;
+      if (tile >= p.max_tiles) break;
+      // a request's last tiles see the most keys: queue them first
+      const int k = find_range(pre_tile, n, i);
+      const int ql = s_ql[k], nt = (ql + p.tile_pos - 1) / p.tile_pos;
+      const int r0 = (nt - 1 - (i - pre_tile[k])) * p.tile_pos;
+      const int npos = min(p.tile_pos, ql - r0), pos0 = (s_len[k] - ql) + r0;
+      p.tiles[2 * tile] = make_int4(base + k, s_q0[k] + r0, npos, pos0);
+      p.tiles[2 * tile + 1] = make_int4(0, pos0 + npos, -1, 1);
+    }
+    carry_full += n_full;
+    carry_rest += static_cast<int>(tot >> 40);
+    carry_tile += n_tile;
+    __syncthreads();  // the prefix arrays are free for the next sweep
+  }
+  if (tid == 0) {
+    int items = all_full + carry_rest;
+    if (static_cast<unsigned long long>(carry_rest) + full_total > static_cast<unsigned long long>(p.max_items)) {
+      flag_error(p.status, PA_FLAG_LENGTHS);
+      items = p.max_items;
+    }
+    p.counts[0] = items;
+    p.counts[1] = p.first_units;
+    p.counts[2] = min(carry_tile, p.max_tiles);
+    p.counts[3] = 0;
+  }
+}
+
+// ---- decode ----------------------------------------------------------------
+
+// A ring tile: 32 rows of D codes, 128-byte swizzle (64-byte at D = 64; rows of
+// head_dim 80 and 96 padded to 128, zero-filled by TMA; head_dim 256 two atoms
+// of 128 codes, atom after atom): eight consecutive rows read at one 16-byte
+// chunk hit eight different bank groups.
+template <int D>
+struct Geom {
+  static constexpr int ROW = D <= 64 ? 64 : 128;
+  static constexpr int ATOMS = D > 128 ? D / 128 : 1;
+  static constexpr int ATOM_BYTES = kTile * ROW;
+  static constexpr int TILE_BYTES = ATOMS * ATOM_BYTES;
+  static constexpr int SLOT_BYTES = 2 * TILE_BYTES;  // K then V
+  static __device__ __forceinline__ uint32_t off(int r, int c) {
+    const uint32_t in_atom = ROW == 128 ? r * 128 + (((c ^ r) & 7) << 4) : r * 64 + (((c ^ (r >> 1)) & 3) << 4);
+    return ATOMS == 1 ? in_atom : (c >> 3) * ATOM_BYTES + in_atom;
+  }
+};
+
+// 4 bytes through L1; src_bytes 0 => zero fill.
+__device__ __forceinline__ void cp_async_4(uint32_t dst, const void *src, int src_bytes) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;\n" ::"r"(dst), "l"(src), "r"(src_bytes) : "memory");
+}
+// One arrival on `bar` (counted in its initial count) once this thread's cp.async copies so far have landed.
+__device__ __forceinline__ void cp_async_mbar_arrive(uint32_t bar) {
+  asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];\n" ::"r"(bar) : "memory");
+}
+__device__ __forceinline__ float4 ld_shared4(uint32_t addr) {
+  float4 v;
+  asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];\n"
+               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+               : "r"(addr)
+               : "memory");
+  return v;
+}
+// Four codes -> fp16 pairs (c0, c1) and (c2, c3), exactly.
+__device__ __forceinline__ void widen_pairs(uint32_t w, uint32_t &p01, uint32_t &p23) {
+  asm("{\n .reg .b16 l, h;\n mov.b32 {l, h}, %2;\n cvt.rn.f16x2.e4m3x2 %0, l;\n cvt.rn.f16x2.e4m3x2 %1, h;\n}\n"
+      : "=r"(p01), "=r"(p23)
+      : "r"(w));
+}
+
+struct Unit {
+  int valid, item, b, row0, nrows, pos0, kv_begin, kv_end, part, kvh, kb0, kb1;
+};
+
+template <int D, int G, int NWARPS, typename E>
+__global__ void __launch_bounds__(NWARPS * 32, 1)
+    block_decode_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap,
+                        const DecodeParams p) {
+  using T = Geom<D>;
+  using M = ElemFp16;                                      // operand type, whatever q is
+  constexpr int S = kRingBytes / (NWARPS * T::SLOT_BYTES);  // ring slots per warp
+  static_assert(S >= 2, "ring needs at least two slots");
+  constexpr int MT = D / 16;
+  // an ldmatrix.x4 covers 32 d, so fragments come in pairs (head_dim 80: one more, all zero)
+  constexpr int MQ = 2 * ((D + 31) / 32);
+  constexpr unsigned FULL = 0xffffffffu;
+
+  extern __shared__ unsigned char smem_raw[];
+  __shared__ __align__(8) uint64_t bars[NWARPS][S];
+  // per slot: K scales of the tile's four 8-key groups, then their V scales
+  __shared__ __align__(16) float scales[NWARPS][S][8];
+  const uint32_t ring = (smem_u32(smem_raw) + 1023u) & ~1023u;
+
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  // a slot's phase: lane 0's expect_tx and the eight scale copies
+  if (threadIdx.x < NWARPS * S) mbar_init(smem_u32(&bars[0][0] + threadIdx.x), 1 + 8);
+  if (threadIdx.x == 0) {
+    prefetch_tmap(&kmap);
+    prefetch_tmap(&vmap);
+  }
+  fence_mbar_init();
+  __syncthreads();
+  griddep_wait();  // the plan (and the cache scatter before it) must be complete
+  if (p.tiles_follow) griddep_launch_dependents();
+
+  const int Hkv = p.num_kv_heads;
+  const int total_units = min(max(ld_cg(p.counts), 0), p.max_items) * Hkv;
+  const uint32_t my_ring = ring + warp * S * T::SLOT_BYTES;
+  const int bs = p.block_size, shift = p.block_shift;
+  const int box_shift = min(shift, 5), box_rows = 1 << box_shift, nbox = kTile >> box_shift;
+
+  auto read_unit = [&](int u) {
+    Unit U;
+    U.valid = u < total_units;
+    U.kb0 = U.kb1 = 0;
+    if (!U.valid) return U;
+    U.item = u / Hkv;
+    U.kvh = u - U.item * Hkv;
+    const int4 r0 = ld_cg(p.items + 2 * U.item);
+    const int4 r1 = ld_cg(p.items + 2 * U.item + 1);
+    U.b = r0.x;
+    U.row0 = r0.y;
+    U.nrows = r0.z;
+    U.pos0 = r0.w;
+    U.kv_begin = r1.x;
+    U.kv_end = r1.y;
+    U.part = r1.z;
+    // a record is trusted only inside the bounds the host passed; else the unit is dropped
+    const bool sane = U.b >= 0 && U.b < p.num_seqs && U.nrows >= 1 && U.nrows <= kCols / G && U.row0 >= 0 &&
+                      U.row0 + U.nrows <= p.total_q && U.kv_begin >= 0 && U.kv_begin % kTile == 0 &&
+                      U.kv_begin < U.kv_end && U.kv_end <= static_cast<int64_t>(p.max_blocks_per_seq) * bs;
+    if (!sane) {
+      if (lane == 0) flag_error(p.status, PA_FLAG_LENGTHS);
+      U.nrows = 0;  // nothing is read or written
+      U.kv_begin = U.kv_end = 0;
+    }
+    U.kb0 = U.kv_begin / kTile;
+    U.kb1 = (U.kv_end + kTile - 1) / kTile;
+    return U;
+  };
+  auto next_unit = [&]() {
+    int u = 0;
+    if (lane == 0) u = atomicAdd(p.counts + 1, 1);
+    return read_unit(__shfl_sync(FULL, u, 0));
+  };
+  // block-table entry of box `lane` of tile kb (negative: no box)
+  auto table_entry = [&](const Unit &U, int kb) {
+    const int key = kb * kTile + lane * box_rows;
+    return lane < nbox && key < U.kv_end
+               ? __ldg(p.block_tables + static_cast<int64_t>(U.b) * p.max_blocks_per_seq + (key >> shift))
+               : -1;
+  };
+
+  // Units are taken in order: `cur` is computed, the producer may be one unit
+  // ahead in `nxt`. phys: table entries of the tile it issues next.
+  Unit cur = read_unit(blockIdx.x + warp * gridDim.x);  // the first without the queue
+  Unit nxt;
+  nxt.valid = 0;
+  bool have_nxt = false, on_nxt = false;
+  int p_kb = cur.kb0;
+  int phys = cur.kb0 < cur.kb1 ? table_entry(cur, cur.kb0) : -1;
+  uint32_t issued = 0, consumed = 0;
+
+  // Stage tile kb of unit U into slot issued % S. Boxes past the unit's end
+  // (or of a block id out of range) are read at a negative row: zero fill.
+  auto issue = [&](const Unit &U, int kb) {
+    const uint32_t slot = issued % S;
+    const uint32_t bar = smem_u32(&bars[warp][slot]);
+    const uint32_t dst = my_ring + slot * T::SLOT_BYTES + lane * box_rows * T::ROW;
+    const int key = kb * kTile + lane * box_rows;  // first key of box `lane`
+    const bool have = lane < nbox && key < U.kv_end;
+    const bool ok = have && phys >= 0 && phys < p.num_blocks;
+    if (have && !ok) flag_error(p.status, PA_FLAG_BLOCK_RANGE);
+    const int z = ok ? (phys << shift) + (key & (bs - 1)) : -box_rows;
+    const int page = ok ? phys : -1;
+    if (lane == 0) mbar_arrive_expect_tx(bar, T::SLOT_BYTES);
+    // scale of group lane % 4: K's in lanes 0-3, V's in 4-7
+    const int gpage = __shfl_sync(FULL, page, ((lane & 3) * 8) >> box_shift);
+    if (lane < 8) {
+      const bool in = gpage >= 0 && kb * kTile + (lane & 3) * 8 < U.kv_end;
+      const float *src = (lane < 4 ? p.k_scales : p.v_scales) + (in ? static_cast<int64_t>(gpage) * Hkv + U.kvh : 0);
+      cp_async_4(smem_u32(&scales[warp][slot][lane]), src, in ? 4 : 0);
+      cp_async_mbar_arrive(bar);
+    }
+    if (lane < nbox) {
+#pragma unroll
+      for (int a = 0; a < T::ATOMS; ++a) {
+        tma_load_3d(dst + a * T::ATOM_BYTES, &kmap, bar, a * 128, U.kvh, z);
+        tma_load_3d(dst + T::TILE_BYTES + a * T::ATOM_BYTES, &vmap, bar, a * 128, U.kvh, z);
+      }
+    }
+    ++issued;
+  };
+  // Issue tiles (cur's, then nxt's) while fewer than `limit` are issued.
+  auto produce = [&](uint32_t limit) {
+    while (issued < limit) {
+      if (!on_nxt && p_kb >= cur.kb1) {
+        if (!have_nxt) {
+          nxt = next_unit();
+          have_nxt = true;
+        }
+        on_nxt = true;
+        p_kb = nxt.kb0;
+        phys = nxt.kb0 < nxt.kb1 ? table_entry(nxt, nxt.kb0) : -1;
+      }
+      const Unit &U = on_nxt ? nxt : cur;
+      if (p_kb >= U.kb1) break;  // at most one unit ahead
+      issue(U, p_kb);
+      ++p_kb;
+      if (p_kb < U.kb1) phys = table_entry(U, p_kb);
+    }
+  };
+
+  const int arow = (lane & 7) + ((lane >> 3) & 1) * 8;  // ldmatrix row of K and V
+
+  while (cur.valid) {
+    // ---- q fragments (B operand of S^T = K Q^T): k step kk pairs d = 16 kk + 4 (lane % 4) + (0, 1) and (2, 3) ----
+    uint32_t qf[MQ][2];
+    float col_scale[2] = {p.scale_log2, p.scale_log2};
+    {
+      const int n = lane >> 2, qi = n / G, g = n % G;
+      const bool ok = qi < cur.nrows;
+      const bf16 *qp = p.q + static_cast<int64_t>(cur.row0 + (ok ? qi : 0)) * p.q_stride +
+                       static_cast<int64_t>(cur.kvh * G + g) * D + 4 * (lane & 3);
+#pragma unroll
+      for (int kk = 0; kk < MQ; ++kk) {
+        const bool in = ok && kk < MT;
+        qf[kk][0] = in ? __ldg(reinterpret_cast<const uint32_t *>(qp + 16 * kk)) : 0u;
+        qf[kk][1] = in ? __ldg(reinterpret_cast<const uint32_t *>(qp + 16 * kk + 2)) : 0u;
+      }
+      if constexpr (std::is_same<E, ElemBf16>::value) {
+        // bf16 -> fp16: a column whose largest |q| reaches 2^15 is first scaled
+        // by 2^-e into [2^14, 2^15), its scores back by 2^e; every value of at
+        // least 2^-17 times the column's scale then converts exactly.
+        float amax = 0.f;
+#pragma unroll
+        for (int kk = 0; kk < MQ; ++kk)
+#pragma unroll
+          for (int h = 0; h < 2; ++h)
+            amax = fmaxf(amax, fmaxf(fabsf(ElemBf16::lo(qf[kk][h])), fabsf(ElemBf16::hi(qf[kk][h]))));
+        amax = fmaxf(amax, __shfl_xor_sync(FULL, amax, 1));
+        amax = fmaxf(amax, __shfl_xor_sync(FULL, amax, 2));
+        const int ex = static_cast<int>((__float_as_uint(amax) >> 23) & 0xffu) - 127;
+        const int e = ex >= 15 ? min(ex - 14, 120) : 0;
+        const float f = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
+#pragma unroll
+        for (int kk = 0; kk < MQ; ++kk)
+#pragma unroll
+          for (int h = 0; h < 2; ++h)
+            qf[kk][h] = ElemFp16::pack(ElemBf16::lo(qf[kk][h]) * f, ElemBf16::hi(qf[kk][h]) * f);
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {  // accumulator column 2 (lane % 4) + j
+          const int ec = __shfl_sync(FULL, e, 4 * (2 * (lane & 3) + j));
+          col_scale[j] = p.scale_log2 * __uint_as_float(static_cast<uint32_t>(127 + ec) << 23);
+        }
+      }
+    }
+    int lim[2];  // keys j < lim[e] are visible to accumulator column 2 (lane % 4) + e
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      const int qi = (2 * (lane & 3) + e) / G;
+      lim[e] = min(cur.pos0 + qi + 1, cur.kv_end);
+    }
+    const int all_see = min(cur.pos0 + 1, cur.kv_end);  // keys every column sees
+    float o[MQ][4];
+#pragma unroll
+    for (int mt = 0; mt < MQ; ++mt) o[mt][0] = o[mt][1] = o[mt][2] = o[mt][3] = 0.f;
+    float m[2] = {-FLT_MAX, -FLT_MAX};  // reference exponents
+    float l[2] = {0.f, 0.f};
+
+    for (int kb = cur.kb0; kb < cur.kb1; ++kb) {
+      produce(consumed + S);
+      const uint32_t slot = consumed % S;
+      const bool landed = mbar_wait_bounded(smem_u32(&bars[warp][slot]), (consumed / S) & 1u, kWaitNs);
+      if (!__all_sync(FULL, landed)) {  // leave together, never with a diverged warp
+        if (lane == 0) {
+          flag_error(p.status, PA_FLAG_TIMEOUT);
+          for (uint32_t g = consumed; g < issued; ++g)  // this warp's loads still in flight
+            (void)mbar_wait_bounded(smem_u32(&bars[warp][g % S]), (g / S) & 1u, kWaitNs);
+        }
+        __syncwarp();
+        return;
+      }
+      const uint32_t kt = my_ring + slot * T::SLOT_BYTES, vt = kt + T::TILE_BYTES;
+      const int key0 = kb * kTile;
+      if (key0 + kTile > cur.kv_end) {  // rows past the last key may hold anything: zero them in V
+        constexpr int CPR = D / 16;
+        const int valid = cur.kv_end - key0, n = (kTile - valid) * CPR;
+        for (int i = lane; i < n; i += 32)
+          asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};\n" ::"r"(vt + T::off(valid + i / CPR, i % CPR)),
+                       "r"(0u)
+                       : "memory");
+        fence_proxy_async_smem();  // before the slot's next TMA fill
+        __syncwarp();
+      }
+      // scores: keys lane / 4 + 8 i (i = 0..3) in s[i / 2][2 (i % 2) + column]
+      float s[2][4];
+      {
+        float sa[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
+        float sb[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
+#pragma unroll
+        for (int j = 0; j < MQ / 2; ++j) {
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            uint32_t r0, r1, r2, r3, a0, a1, a2, a3;
+            ldsm_x4(kt + h * 16 * T::ROW + T::off(arow, 2 * j + (lane >> 4)), r0, r1, r2, r3);
+            widen_pairs(r0, a0, a2);
+            widen_pairs(r1, a1, a3);
+            M::mma(sa[h], a0, a1, a2, a3, qf[2 * j][0], qf[2 * j][1]);
+            widen_pairs(r2, a0, a2);
+            widen_pairs(r3, a1, a3);
+            M::mma(sb[h], a0, a1, a2, a3, qf[2 * j + 1][0], qf[2 * j + 1][1]);
+          }
+        }
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) s[h][i] = sa[h][i] + sb[h][i];
+      }
+      const float4 k4 = ld_shared4(smem_u32(&scales[warp][slot][0]));
+      const float4 v4 = ld_shared4(smem_u32(&scales[warp][slot][4]));
+      const float gk[4] = {k4.x, k4.y, k4.z, k4.w}, gv[4] = {v4.x, v4.y, v4.z, v4.w};
+      if (key0 + kTile > all_see) {  // a unit's last tiles: keys some column does not see
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+          for (int c = 0; c < 2; ++c)
+            if (key0 + 8 * i + (lane >> 2) >= lim[c]) s[i >> 1][2 * (i & 1) + c] = -INFINITY;
+      }
+      float e[4][2], glv[4];
+      float top = -INFINITY;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        glv[i] = __log2f(gv[i]);
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          // a group past the last key has scales 0: its (masked) scores stay -inf
+          const float f = gk[i] > 0.f ? col_scale[c] * gk[i] : 1.f;
+          const float x = s[i >> 1][2 * (i & 1) + c];
+          e[i][c] = fmaf(x, f, glv[i] - m[c]);
+          top = fmaxf(top, e[i][c]);
+        }
+      }
+      if (__any_sync(FULL, top > kGrowLog2)) {
+        // move the references to the columns' maxima (lanes of one column agree)
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          float mx = -INFINITY;
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const float f = gk[i] > 0.f ? col_scale[c] * gk[i] : 1.f;
+            e[i][c] = __fadd_rn(__fmul_rn(s[i >> 1][2 * (i & 1) + c], f), glv[i]);
+            mx = fmaxf(mx, e[i][c]);
+          }
+#pragma unroll
+          for (int off = 4; off < 32; off <<= 1) mx = fmaxf(mx, __shfl_xor_sync(FULL, mx, off));
+          const float mn = fmaxf(m[c], mx);
+          const float al = ex2_approx(m[c] - mn);
+          m[c] = mn;
+          l[c] *= al;
+#pragma unroll
+          for (int mt = 0; mt < MQ; ++mt) {
+            o[mt][c] *= al;
+            o[mt][2 + c] *= al;
+          }
+#pragma unroll
+          for (int i = 0; i < 4; ++i) e[i][c] = __fsub_rn(e[i][c], mn);
+        }
+      }
+      uint32_t pk[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const float inv = gv[i] > 0.f ? __fdividef(1.f, gv[i]) : 0.f;
+        const float p0 = ex2_approx(e[i][0]), p1 = ex2_approx(e[i][1]);
+        l[0] = fmaf(p0, inv, l[0]);
+        l[1] = fmaf(p1, inv, l[1]);
+        pk[i] = movmatrix_t(M::pack(p0, p1));
+      }
+      // O^T += V^T P^T: row lane / 4 of m tile mt holds d = 16 mt + 2 (lane / 4), row lane / 4 + 8 the next one
+#pragma unroll
+      for (int j = 0; j < MQ / 2; ++j) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          uint32_t r0, r1, r2, r3, l0, h0, l1, h1;
+          ldsm_x4_t(vt + h * 16 * T::ROW + T::off(arow, 2 * j + (lane >> 4)), r0, r1, r2, r3);
+          M::from_e4m3x4(r0, l0, h0);
+          M::from_e4m3x4(r1, l1, h1);
+          M::mma(o[2 * j], l0, h0, l1, h1, pk[2 * h], pk[2 * h + 1]);
+          M::from_e4m3x4(r2, l0, h0);
+          M::from_e4m3x4(r3, l1, h1);
+          M::mma(o[2 * j + 1], l0, h0, l1, h1, pk[2 * h], pk[2 * h + 1]);
+        }
+      }
+      __syncwarp();  // every lane is done with the slot before it is refilled
+      ++consumed;
+    }
+
+    // ---- epilogue: normalise, write the output or the partial ----
+    if (cur.nrows > 0) {
+#pragma unroll
+      for (int off = 4; off < 32; off <<= 1) {
+        l[0] += __shfl_xor_sync(FULL, l[0], off);
+        l[1] += __shfl_xor_sync(FULL, l[1], off);
+      }
+      const float inv0 = l[0] > 0.f ? 1.f / l[0] : 0.f;
+      const float inv1 = l[1] > 0.f ? 1.f / l[1] : 0.f;
+      if (cur.part < 0) {
+        const int col = lane >> 2, qi = col / G, g = col % G;
+        bf16 *dst = p.out + static_cast<int64_t>(cur.row0 + (qi < cur.nrows ? qi : 0)) * p.num_heads * D +
+                    static_cast<int64_t>(cur.kvh * G + g) * D;
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt) {
+          // transposed, lo8 holds d = 16 mt + 4 (lane % 4) + (0, 2) of one column, hi8 (1, 3)
+          const uint32_t lo8 = movmatrix_t(E::pack(o[mt][0] * inv0, o[mt][1] * inv1));
+          const uint32_t hi8 = movmatrix_t(E::pack(o[mt][2] * inv0, o[mt][3] * inv1));
+          if (qi < cur.nrows)
+            *reinterpret_cast<uint2 *>(dst + 16 * mt + 4 * (lane & 3)) =
+                make_uint2(__byte_perm(lo8, hi8, 0x5410), __byte_perm(lo8, hi8, 0x7632));
+        }
+      } else {
+        const int64_t base = (static_cast<int64_t>(cur.item) * Hkv + cur.kvh) * kCols;
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          const int col = 2 * (lane & 3) + c;
+          if (col / G < cur.nrows) {
+            const float inv = c ? inv1 : inv0;
+            float *dst = p.part_o + (base + col) * D + 2 * (lane >> 2);
+#pragma unroll
+            for (int mt = 0; mt < MT; ++mt)
+              *reinterpret_cast<float2 *>(dst + 16 * mt) = make_float2(o[mt][c] * inv, o[mt][2 + c] * inv);
+            if (lane < 4) p.part_lse[base + col] = l[c] > 0.f ? m[c] + __log2f(l[c]) : -INFINITY;
+          }
+        }
+      }
+    }
+
+    // ---- the next unit (the producer may already be streaming it) ----
+    if (!have_nxt) nxt = next_unit();
+    if (!on_nxt) {
+      p_kb = nxt.kb0;
+      phys = nxt.kb0 < nxt.kb1 ? table_entry(nxt, nxt.kb0) : -1;
+    }
+    cur = nxt;
+    have_nxt = on_nxt = false;
+  }
+}
+
+// ---- merge -----------------------------------------------------------------
+
+// One CTA of eight warps per (request, KV head): the used columns (query rows
+// x G, at most 8) rounded up to a power of two NC take a warp each, and the
+// 8 / NC warps of a column share its partitions in contiguous runs, joined
+// through shared memory in order (the same bits every time). A warp reads
+// eight partitions at a time with a running maximum of their log-sum-exps.
+template <int D, int G, typename E>
+__global__ void __launch_bounds__(256) block_merge_kernel(const MergeParams p) {
+  constexpr int EPL = (D + 31) / 32;  // outputs per lane (head_dim 80, 96: the last lanes' unused)
+  constexpr bool VEC4 = D % 128 == 0, VEC2 = D == 64;
+  __shared__ float s_m[kCols], s_w[kCols], s_acc[kCols][32 * EPL];
+  griddep_wait();
+  griddep_launch_dependents();
+  const int b = blockIdx.x / p.num_kv_heads, kvh = blockIdx.x - b * p.num_kv_heads;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int np = ld_cg(p.nparts + b), full0 = ld_cg(p.first_full + b), rest = ld_cg(p.rest + b);
+  const int q0 = ld_cg(p.query_start_loc + b), ql = ld_cg(p.query_start_loc + b + 1) - q0;
+  if (np <= 1 || ql < 1 || ql * G > kCols) return;
+  const int cols = ql * G;
+  const int nc = cols <= 1 ? 1 : (cols <= 2 ? 2 : (cols <= 4 ? 4 : 8));
+  const int col = warp % nc, sub = warp / nc, subs = kCols / nc;
+  const int k_begin = np * sub / subs, k_end = np * (sub + 1) / subs;
+  float M = -INFINITY, wsum = 0.f, acc[EPL];
+#pragma unroll
+  for (int e = 0; e < EPL; ++e) acc[e] = 0.f;
+  if (col < cols) {
+    for (int k0 = k_begin; k0 < k_end; k0 += 8) {
+      float lv[8], ov[8][EPL];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const int k = min(k0 + j, k_end - 1);
+        const int item = min(max(k == np - 1 && rest >= 0 ? rest : full0 + k, 0), p.max_items - 1);
+        const int64_t at = (static_cast<int64_t>(item) * p.num_kv_heads + kvh) * kCols + col;
+        lv[j] = ld_cg(p.part_lse + at);
+        const float *src = p.part_o + at * D + lane * EPL;
+        if constexpr (VEC2) {
+          const float2 v = ld_cg(reinterpret_cast<const float2 *>(src));
+          ov[j][0] = v.x, ov[j][1] = v.y;
+        } else if constexpr (VEC4) {
+#pragma unroll
+          for (int e = 0; e < EPL; e += 4) {
+            const float4 v = ld_cg(reinterpret_cast<const float4 *>(src + e));
+            ov[j][e] = v.x, ov[j][e + 1] = v.y, ov[j][e + 2] = v.z, ov[j][e + 3] = v.w;
+          }
+        } else {
+#pragma unroll
+          for (int e = 0; e < EPL; ++e) ov[j][e] = lane * EPL + e < D ? ld_cg(src + e) : 0.f;
+        }
+      }
+      float Mn = M;
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        if (k0 + j < k_end) Mn = fmaxf(Mn, lv[j]);
+      const float Ms = Mn == -INFINITY ? 0.f : Mn;
+      const float r = ex2_approx(M - Ms);
+      wsum *= r;
+#pragma unroll
+      for (int e = 0; e < EPL; ++e) acc[e] *= r;
+      M = Mn;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        if (k0 + j < k_end) {
+          const float w = ex2_approx(lv[j] - Ms);
+          wsum += w;
+#pragma unroll
+          for (int e = 0; e < EPL; ++e) acc[e] += w * ov[j][e];
+        }
+      }
+    }
+  }
+  if (subs > 1) {
+    if (lane == 0) {
+      s_m[warp] = M;
+      s_w[warp] = wsum;
+    }
+#pragma unroll
+    for (int e = 0; e < EPL; ++e) s_acc[warp][e * 32 + lane] = acc[e];
+    __syncthreads();
+    if (sub > 0) return;
+    for (int k = 1; k < subs; ++k) {
+      const int w = k * nc + col;
+      const float Mo = s_m[w], Mn = fmaxf(M, Mo), Ms = Mn == -INFINITY ? 0.f : Mn;
+      const float ra = ex2_approx(M - Ms), rb = ex2_approx(Mo - Ms);
+      wsum = wsum * ra + s_w[w] * rb;
+#pragma unroll
+      for (int e = 0; e < EPL; ++e) acc[e] = acc[e] * ra + s_acc[w][e * 32 + lane] * rb;
+      M = Mn;
+    }
+  }
+  if (col >= cols) return;
+  const float inv = wsum > 0.f ? 1.f / wsum : 0.f;
+  bf16 *dst = p.out + static_cast<int64_t>(q0 + col / G) * p.num_heads * D +
+              static_cast<int64_t>(kvh * G + col % G) * D + lane * EPL;
+  if constexpr (VEC2) {
+    *reinterpret_cast<uint32_t *>(dst) = E::pack(acc[0] * inv, acc[1] * inv);
+  } else if constexpr (VEC4) {
+#pragma unroll
+    for (int e = 0; e < EPL; e += 4)
+      *reinterpret_cast<uint2 *>(dst + e) =
+          make_uint2(E::pack(acc[e] * inv, acc[e + 1] * inv), E::pack(acc[e + 2] * inv, acc[e + 3] * inv));
+  } else {
+#pragma unroll
+    for (int e = 0; e < EPL; ++e)
+      if (lane * EPL + e < D)
+        *reinterpret_cast<unsigned short *>(dst + e) =
+            static_cast<unsigned short>(E::pack(acc[e] * inv, 0.f) & 0xffffu);
+  }
+}
+
+// ---- host ------------------------------------------------------------------
+
+size_t align256(size_t x) { return (x + 255) & ~static_cast<size_t>(255); }
+
+PFN_cuTensorMapEncodeTiled_v12000 map_encoder() {
+  static std::once_flag once;
+  static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
+  std::call_once(once, []() {
+    void *ptr = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &ptr, 12000, cudaEnableDefault, &q) ==
+            cudaSuccess &&
+        q == cudaDriverEntryPointSuccess)
+      fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(ptr);
+  });
+  return fn;
+}
+
+// 3-D view of one cache of codes, [num_blocks * block_size rows][Hkv][D], with
+// a box of min(block_size, 32) rows x 1 head x 64 or 128 codes.
+bool encode_map(CUtensorMap *map, const void *cache, int64_t num_blocks, int32_t num_kv_heads, int32_t head_dim,
+                int32_t block_size) {
+  auto encode = map_encoder();
+  if (!encode) return false;
+  const cuuint64_t dims[3] = {static_cast<cuuint64_t>(head_dim), static_cast<cuuint64_t>(num_kv_heads),
+                              static_cast<cuuint64_t>(num_blocks) * block_size};
+  const cuuint64_t strides[2] = {static_cast<cuuint64_t>(head_dim),
+                                 static_cast<cuuint64_t>(num_kv_heads) * head_dim};
+  const cuuint32_t box[3] = {head_dim <= 64 ? 64u : 128u, 1,
+                             static_cast<cuuint32_t>(block_size < kTile ? block_size : kTile)};
+  const cuuint32_t estr[3] = {1, 1, 1};
+  return encode(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<void *>(cache), dims, strides, box, estr,
+                CU_TENSOR_MAP_INTERLEAVE_NONE,
+                head_dim <= 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B,
+                CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <int D, int G, typename E>
+cudaError_t launch_typed(const AttnLaunch &a, const BlockWorkspace &w, cudaStream_t stream, int *launched) {
+  char *ws = static_cast<char *>(a.workspace);
+  constexpr int NW = block_warps(D);
+  CUtensorMap kmap, vmap;
+  if (!encode_map(&kmap, a.key_cache, a.num_blocks, a.num_kv_heads, D, a.block_size) ||
+      !encode_map(&vmap, a.value_cache, a.num_blocks, a.num_kv_heads, D, a.block_size))
+    return cudaErrorInvalidValue;
+  const int64_t units_upper = static_cast<int64_t>(w.max_items) * a.num_kv_heads;
+  const int64_t grid = units_upper < a.sm_count ? units_upper : a.sm_count;  // one CTA per SM
+
+  PlanParams pp;
+  pp.seq_lens = a.seq_lens;
+  pp.query_start_loc = a.query_start_loc;
+  pp.num_seqs = a.num_seqs;
+  pp.total_q = a.total_q;
+  pp.max_query_len = a.max_query_len;
+  pp.max_seq_len = a.max_seq_len;
+  pp.max_blocks_per_seq = a.max_blocks_per_seq;
+  pp.block_size = a.block_size;
+  pp.num_kv_heads = a.num_kv_heads;
+  pp.rows_per_item = kCols / G;
+  pp.tile_pos = prefill_tile_rows(D) / G;
+  pp.max_items = w.max_items;
+  pp.max_tiles = w.max_tiles;
+  pp.warps = unit_warps(D);
+  pp.first_units = static_cast<int32_t>(grid * NW);
+  pp.nparts = reinterpret_cast<int32_t *>(ws + w.nparts);
+  pp.first_full = reinterpret_cast<int32_t *>(ws + w.first_full);
+  pp.rest = reinterpret_cast<int32_t *>(ws + w.rest);
+  pp.counts = reinterpret_cast<int32_t *>(ws + w.counts);
+  pp.items = reinterpret_cast<int4 *>(ws + w.items);
+  pp.tiles = reinterpret_cast<int4 *>(ws + w.tiles);
+  pp.status = a.status;
+  cudaError_t err = a.num_seqs <= 256 ? launch_pdl(block_plan_kernel<256>, dim3(1), dim3(256), 0, stream, pp)
+                                      : launch_pdl(block_plan_kernel<1024>, dim3(1), dim3(1024), 0, stream, pp);
+  if (err != cudaSuccess) return err;
+  ++*launched;
+
+  const bool tiles_follow = a.max_query_len > pp.rows_per_item;
+  DecodeParams dp;
+  dp.q = static_cast<const bf16 *>(a.q);
+  dp.q_stride = a.q_stride;
+  dp.block_tables = a.block_tables;
+  dp.max_blocks_per_seq = a.max_blocks_per_seq;
+  dp.block_size = a.block_size;
+  dp.block_shift = a.block_size == 8 ? 3 : (a.block_size == 16 ? 4 : 5);
+  dp.num_heads = a.num_heads;
+  dp.num_kv_heads = a.num_kv_heads;
+  dp.num_blocks = a.num_blocks;
+  dp.k_scales = a.k_scales;
+  dp.v_scales = a.v_scales;
+  dp.scale_log2 = a.scale * 1.4426950408889634f;
+  dp.out = static_cast<bf16 *>(a.out);
+  dp.items = pp.items;
+  dp.counts = pp.counts;
+  dp.num_seqs = a.num_seqs;
+  dp.total_q = a.total_q;
+  dp.max_items = w.max_items;
+  dp.part_o = reinterpret_cast<float *>(ws + w.part_o);
+  dp.part_lse = reinterpret_cast<float *>(ws + w.part_lse);
+  dp.tiles_follow = tiles_follow ? 1 : 0;
+  dp.status = a.status;
+  constexpr int smem = kRingBytes + 1024;  // ring + alignment slack
+  auto kern = block_decode_kernel<D, G, NW, E>;
+  err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (err != cudaSuccess) return err;
+  err = cudaFuncSetAttribute(kern, cudaFuncAttributePreferredSharedMemoryCarveout, 100);
+  if (err != cudaSuccess) return err;
+  if (a.ev_start) cudaEventRecord(a.ev_start, stream);
+  err = launch_pdl(kern, dim3(static_cast<unsigned>(grid)), dim3(NW * 32), smem, stream, kmap, vmap, dp);
+  if (err != cudaSuccess) return err;
+  ++*launched;
+  if (a.ev_stop) cudaEventRecord(a.ev_stop, stream);
+
+  if (tiles_follow) {  // some request may be a prefill chunk
+    TileParams tp;
+    tp.q = dp.q;
+    tp.q_stride = a.q_stride;
+    tp.block_tables = a.block_tables;
+    tp.max_blocks_per_seq = a.max_blocks_per_seq;
+    tp.block_size = a.block_size;
+    tp.block_shift = dp.block_shift;
+    tp.num_heads = a.num_heads;
+    tp.num_kv_heads = a.num_kv_heads;
+    tp.num_blocks = a.num_blocks;
+    tp.scale_log2 = dp.scale_log2;
+    tp.out_scale = 1.0f;
+    tp.out = dp.out;
+    tp.tiles = pp.tiles;
+    tp.tile_count = pp.counts + 2;
+    tp.tile_counter = pp.counts + 3;
+    tp.num_seqs = a.num_seqs;
+    tp.total_q = a.total_q;
+    tp.max_tiles = w.max_tiles;
+    tp.k_scales = a.k_scales;
+    tp.v_scales = a.v_scales;
+    tp.status = a.status;
+    if (a.tile_start) cudaEventRecord(a.tile_start, stream);
+    err = launch_prefill_tiles<D, G, E, true, true>(kmap, vmap, vmap, tp, a.sm_count, stream);
+    if (err != cudaSuccess) return err;
+    if (a.tile_stop) cudaEventRecord(a.tile_stop, stream);
+    ++*launched;
+  }
+
+  if (a.max_seq_len > kTile) {  // some request may be split
+    MergeParams mp;
+    mp.query_start_loc = a.query_start_loc;
+    mp.nparts = pp.nparts;
+    mp.first_full = pp.first_full;
+    mp.rest = pp.rest;
+    mp.num_kv_heads = a.num_kv_heads;
+    mp.num_heads = a.num_heads;
+    mp.max_items = w.max_items;
+    mp.part_o = dp.part_o;
+    mp.part_lse = dp.part_lse;
+    mp.out = dp.out;
+    err = launch_pdl(block_merge_kernel<D, G, E>, dim3(static_cast<unsigned>(a.num_seqs * a.num_kv_heads)), dim3(256),
+                     0, stream, mp);
+    if (err != cudaSuccess) return err;
+    ++*launched;
+  }
+  return cudaSuccess;
+}
+
+}  // namespace
+
+bool block_workspace_layout(int32_t num_seqs, int32_t total_q, int32_t max_seq_len, int32_t num_heads,
+                            int32_t num_kv_heads, int32_t head_dim, BlockWorkspace &w) {
+  if (num_seqs < 0 || total_q < 0 || max_seq_len < 0 || num_heads <= 0 || num_kv_heads <= 0 || head_dim <= 0 ||
+      num_heads % num_kv_heads != 0 || num_heads / num_kv_heads > kCols)
+    return false;
+  const int G = num_heads / num_kv_heads;
+  // a request of t key tiles gives at most t / U + 1 items, U >= total / (kUnitsPerWarp * warps)
+  const int64_t key_tiles = (static_cast<int64_t>(max_seq_len) + kTile - 1) / kTile;
+  const int64_t full = (kUnitsPerWarp * unit_warps(head_dim) + num_kv_heads - 1) / num_kv_heads;
+  int64_t items = static_cast<int64_t>(num_seqs) * key_tiles;
+  if (items > num_seqs + full) items = num_seqs + full;
+  const int rows = prefill_tile_rows(head_dim);
+  const int64_t tiles = (static_cast<int64_t>(total_q) * G + rows - 1) / rows + num_seqs;
+  if (items * num_kv_heads > (1LL << 30) || tiles * num_kv_heads > (1LL << 30) ||
+      static_cast<int64_t>(num_seqs) * num_kv_heads > (1LL << 30))
+    return false;
+  w.max_items = static_cast<int32_t>(items > 0 ? items : 1);
+  w.max_tiles = static_cast<int32_t>(tiles > 0 ? tiles : 1);
+  const size_t per_seq = align256(sizeof(int32_t) * (static_cast<size_t>(num_seqs) + 1));
+  const size_t parts = static_cast<size_t>(w.max_items) * num_kv_heads * kCols;
+  size_t off = 0;
+  w.counts = off;     off += 256;
+  w.nparts = off;     off += per_seq;
+  w.first_full = off; off += per_seq;
+  w.rest = off;       off += per_seq;
+  w.items = off;      off += align256(sizeof(int4) * 2 * static_cast<size_t>(w.max_items));
+  w.tiles = off;      off += align256(sizeof(int4) * 2 * static_cast<size_t>(w.max_tiles));
+  w.part_lse = off;   off += align256(sizeof(float) * parts);
+  w.part_o = off;     off += align256(sizeof(float) * parts * head_dim);
+  w.total = off;
+  return true;
+}
+
+cudaError_t launch_block_attention(const AttnLaunch &a, cudaStream_t stream, int *launched) {
+  BlockWorkspace w;
+  if (!block_workspace_layout(a.num_seqs, a.total_q, a.max_seq_len, a.num_heads, a.num_kv_heads, a.head_dim, w))
+    return cudaErrorInvalidValue;
+  const int G = a.num_heads / a.num_kv_heads;
+#define PA_DISPATCH(DD, GG)                                                               \
+  if (a.head_dim == DD && G == GG)                                                        \
+    return a.dtype == PA_FP16 ? launch_typed<DD, GG, ElemFp16>(a, w, stream, launched)    \
+                              : launch_typed<DD, GG, ElemBf16>(a, w, stream, launched);
+  PA_DISPATCH(128, 1) PA_DISPATCH(128, 2) PA_DISPATCH(128, 4) PA_DISPATCH(128, 8)
+  PA_DISPATCH(64, 1) PA_DISPATCH(64, 2) PA_DISPATCH(64, 4) PA_DISPATCH(64, 8)
+  PA_DISPATCH(96, 1) PA_DISPATCH(96, 2) PA_DISPATCH(96, 4) PA_DISPATCH(96, 8)
+  PA_DISPATCH(80, 1) PA_DISPATCH(80, 2) PA_DISPATCH(80, 4) PA_DISPATCH(80, 8)
+  PA_DISPATCH(256, 1) PA_DISPATCH(256, 2) PA_DISPATCH(256, 4) PA_DISPATCH(256, 8)
+#undef PA_DISPATCH
+  return cudaErrorInvalidValue;
+}
+
+}  // namespace pa

@@ -40,8 +40,8 @@ struct TileParams {
   int32_t num_seqs;
   int32_t total_q;
   int32_t max_tiles;
-  const float *k_scales;  // 8-bit caches with block scales: [num_blocks][Hkv]
-  const float *v_scales;
+  const float *k_scales = nullptr;  // 8-bit caches with block scales: [num_blocks][Hkv]
+  const float *v_scales = nullptr;
   unsigned int *status;
 };
 
@@ -52,7 +52,7 @@ struct TileParams {
 // KV head) instead of one per cache.
 // vmapb: at head_dim 128 over 16-bit caches, the value cache as whole-block
 // boxes (block_size rows x both 64-element atoms; unused otherwise).
-template <int D, int G, typename E, bool KV8, bool BSC>
+template <int D, int G, typename E, bool KV8, bool BSC = false>
 cudaError_t launch_prefill_tiles(const CUtensorMap &kmap, const CUtensorMap &vmap, const CUtensorMap &vmapb,
                                  const TileParams &tp, int sm_count, cudaStream_t stream);
 

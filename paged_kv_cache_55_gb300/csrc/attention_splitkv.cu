@@ -105,8 +105,6 @@ struct AttnParams {
   float *part_lse;  // [num_seqs][Hkv][max_parts][8]
   int32_t block_boxes;  // 1: 16-bit caches, head_dim 128, blocks of >= 16 tokens: one 4-D box per tile
   int32_t tiles_follow; // 1: the prefill-tile kernel is launched after this one
-  const float *k_scales;  // 8-bit caches with block scales: [num_blocks][Hkv]
-  const float *v_scales;
   unsigned int *status;
 };
 
@@ -572,19 +570,7 @@ struct TileGeom<D, true> {
   }
 };
 
-// 8-bit caches with block scales (BSC): a block's keys are worth code * ks and
-// its values code * vs, ks and vs the block's scales for this KV head. ks
-// multiplies the scores. vs is folded into the exponent: with
-// x_j = s_j ks + log2 vs and m the running maximum of x, P'_j = 2^(x_j - m)
-// lies in (0, 1] whatever the scales are (so it fits the fp16 operand), and
-//   O = sum_j P'_j code_j,  l = sum_j P'_j / vs_j,  out = O / l,
-// since P'_j / vs_j = 2^(s_j ks - m) is the plain softmax weight; the
-// partial's log-sum-exp is m + log2 l as before. One maximum and one exponent
-// per score: the cost over one scale per cache is a multiply-add per score
-// and a scaled sum. The scales of a tile travel with it: lanes 0..7 copy the
-// eight floats of its four 8-key groups into the slot with cp.async, counted
-// on the slot's mbarrier like the TMA boxes.
-template <int D, int G, int NWARPS, typename E, bool KV8, bool BSC>
+template <int D, int G, int NWARPS, typename E, bool KV8>
 __global__ void __launch_bounds__(NWARPS * 32, 1)
     splitkv_attention_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap,
                              const __grid_constant__ CUtensorMap kmap4, const __grid_constant__ CUtensorMap vmap4,
@@ -597,7 +583,6 @@ __global__ void __launch_bounds__(NWARPS * 32, 1)
   constexpr int KT = KV8 ? kTileKeys8 : kTileKeys;            // keys per ring tile
   constexpr int S = kSmemBudget / (NWARPS * T::SLOT_BYTES);  // ring slots per warp
   static_assert(S >= 2, "ring needs at least two slots");
-  static_assert(KV8 || !BSC, "block scales belong to 8-bit caches");
   constexpr int MT = D / 16;  // k steps of S, m tiles of O
   // 8-bit caches: an ldmatrix.x4 covers 32 d, so fragments come in pairs; a
   // head_dim of 80 computes one more (all-zero) k step and m tile
@@ -605,12 +590,10 @@ __global__ void __launch_bounds__(NWARPS * 32, 1)
 
   extern __shared__ unsigned char smem_raw[];
   __shared__ __align__(8) uint64_t bars[NWARPS][S];
-  // per slot: K scales of the tile's four 8-key groups, then their V scales
-  __shared__ __align__(16) float scales[BSC ? NWARPS : 1][S][8];
   const uint32_t ring = (smem_u32(smem_raw) + 1023u) & ~1023u;
 
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  if (threadIdx.x < NWARPS * S) mbar_init(smem_u32(&bars[0][0] + threadIdx.x), BSC ? 1 + 8 : 1);
+  if (threadIdx.x < NWARPS * S) mbar_init(smem_u32(&bars[0][0] + threadIdx.x), 1);
   if (threadIdx.x == 0) {
     prefetch_tmap(&kmap);
     prefetch_tmap(&vmap);
@@ -639,24 +622,6 @@ __global__ void __launch_bounds__(NWARPS * 32, 1)
   // block-table entry is read only for a block that holds a key below the
   // unit's end; boxes past it are read at a negative row (zero fill).
   auto issue = [&](const Unit &U, int kb, uint32_t seq) {
-    if constexpr (BSC) {
-      if (lane < 8) {  // group lane % 4 of the tile: its K scale (lanes 0-3) or V scale (lanes 4-7)
-        const uint32_t slot = seq % S;
-        const int key = kb * KT + (lane & 3) * 8;
-        const float *src = lane < 4 ? p.k_scales : p.v_scales;
-        int bytes = 0;  // groups past the unit's end: zero
-        if (key < U.kv_end) {
-          const int phys = __ldg(p.block_tables + static_cast<int64_t>(U.b) * p.max_blocks_per_seq +
-                                 (key >> p.block_shift));
-          if (phys >= 0 && phys < p.num_blocks) {
-            src += static_cast<int64_t>(phys) * Hkv + U.kvh;
-            bytes = 4;
-          }
-        }
-        cp_async_4(smem_u32(&scales[warp][slot][lane]), src, bytes);
-        cp_async_mbar_arrive(smem_u32(&bars[warp][slot]));
-      }
-    }
     if (lane == 0) {
       const uint32_t slot = seq % S;
       const uint32_t bar = smem_u32(&bars[warp][slot]);
@@ -930,33 +895,14 @@ __global__ void __launch_bounds__(NWARPS * 32, 1)
       scores(kt0, s0);
       if (two) scores(kt1, s1);
       const int t0 = kb * KT + (lane >> 2), t1 = t0 + 8, t2 = t0 + kTileKeys, t3 = t1 + kTileKeys;
-      // block scales of the 8-key groups that t0 .. t3 belong to: K's, log2 and inverse of V's
-      float gk[4], glv[4], giv[4];
-      if constexpr (BSC) {
-        const float4 k4 = ld_shared4(&scales[warp][consumed % S][0]);
-        const float4 v4 = ld_shared4(&scales[warp][consumed % S][4]);
-        gk[0] = k4.x, gk[1] = k4.y, gk[2] = k4.z, gk[3] = k4.w;
-        const float v[4] = {v4.x, v4.y, v4.z, v4.w};
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          glv[i] = __log2f(v[i]);
-          giv[i] = v[i] > 0.f ? __fdividef(1.f, v[i]) : 0.f;  // 0: a group past the end
-        }
-      }
-      auto logit = [&](float s, int col, int grp) -> float {
-        if constexpr (BSC)
-          return __fadd_rn(__fmul_rn(s, __fmul_rn(col_scale[col], gk[grp])), glv[grp]);
-        else
-          return __fmul_rn(s, col_scale[col]);
-      };
-      const float x0 = t0 < lim[0] ? logit(s0[0], 0, 0) : -INFINITY;
-      const float x1 = t0 < lim[1] ? logit(s0[1], 1, 0) : -INFINITY;
-      const float x2 = t1 < lim[0] ? logit(s0[2], 0, 1) : -INFINITY;
-      const float x3 = t1 < lim[1] ? logit(s0[3], 1, 1) : -INFINITY;
-      const float y0 = two && t2 < lim[0] ? logit(s1[0], 0, 2) : -INFINITY;
-      const float y1 = two && t2 < lim[1] ? logit(s1[1], 1, 2) : -INFINITY;
-      const float y2 = two && t3 < lim[0] ? logit(s1[2], 0, 3) : -INFINITY;
-      const float y3 = two && t3 < lim[1] ? logit(s1[3], 1, 3) : -INFINITY;
+      const float x0 = t0 < lim[0] ? __fmul_rn(s0[0], col_scale[0]) : -INFINITY;
+      const float x1 = t0 < lim[1] ? __fmul_rn(s0[1], col_scale[1]) : -INFINITY;
+      const float x2 = t1 < lim[0] ? __fmul_rn(s0[2], col_scale[0]) : -INFINITY;
+      const float x3 = t1 < lim[1] ? __fmul_rn(s0[3], col_scale[1]) : -INFINITY;
+      const float y0 = two && t2 < lim[0] ? __fmul_rn(s1[0], col_scale[0]) : -INFINITY;
+      const float y1 = two && t2 < lim[1] ? __fmul_rn(s1[1], col_scale[1]) : -INFINITY;
+      const float y2 = two && t3 < lim[0] ? __fmul_rn(s1[2], col_scale[0]) : -INFINITY;
+      const float y3 = two && t3 < lim[1] ? __fmul_rn(s1[3], col_scale[1]) : -INFINITY;
       // rounded products (never contracted into the subtractions below), so the
       // maximum's exponent is exactly zero whatever the magnitude of the scores
       float mx0 = fmaxf(fmaxf(x0, x2), fmaxf(y0, y2)), mx1 = fmaxf(fmaxf(x1, x3), fmaxf(y1, y3));
@@ -973,13 +919,8 @@ __global__ void __launch_bounds__(NWARPS * 32, 1)
       const float p2 = ex2_approx(x2 - ms0), p3 = ex2_approx(x3 - ms1);
       const float q0 = ex2_approx(y0 - ms0), q1 = ex2_approx(y1 - ms1);
       const float q2 = ex2_approx(y2 - ms0), q3 = ex2_approx(y3 - ms1);
-      if constexpr (BSC) {
-        l[0] = l[0] * al0 + (fmaf(p0, giv[0], p2 * giv[1]) + fmaf(q0, giv[2], q2 * giv[3]));
-        l[1] = l[1] * al1 + (fmaf(p1, giv[0], p3 * giv[1]) + fmaf(q1, giv[2], q3 * giv[3]));
-      } else {
-        l[0] = l[0] * al0 + ((p0 + p2) + (q0 + q2));
-        l[1] = l[1] * al1 + ((p1 + p3) + (q1 + q3));
-      }
+      l[0] = l[0] * al0 + ((p0 + p2) + (q0 + q2));
+      l[1] = l[1] * al1 + ((p1 + p3) + (q1 + q3));
       m[0] = mn0;
       m[1] = mn1;
       if (__any_sync(0xffffffffu, al0 != 1.f || al1 != 1.f)) {
@@ -1212,7 +1153,7 @@ constexpr int decode_warps() {
   return D == 256 ? 4 : (KV8 ? kAttnWarps8 : kAttnWarps);
 }
 
-template <int D, int G, typename E, bool KV8, bool BSC>
+template <int D, int G, typename E, bool KV8>
 static cudaError_t launch_typed(const AttnLaunch &a, const WorkspaceLayout &w, cudaStream_t stream,
                                 int *launched) {
   char *ws = static_cast<char *>(a.workspace);
@@ -1281,13 +1222,11 @@ static cudaError_t launch_typed(const AttnLaunch &a, const WorkspaceLayout &w, c
   ap.part_lse = reinterpret_cast<float *>(ws + w.part_lse);
   ap.block_boxes = block_boxes ? 1 : 0;
   ap.tiles_follow = a.max_query_len > w.rows_per_item ? 1 : 0;
-  ap.k_scales = a.k_scales;
-  ap.v_scales = a.v_scales;
   ap.status = a.status;
 
   constexpr int smem = kSmemBudget + 1024;  // ring + alignment slack
   constexpr int NW = decode_warps<D, KV8>();
-  auto kern = splitkv_attention_kernel<D, G, NW, E, KV8, BSC>;
+  auto kern = splitkv_attention_kernel<D, G, NW, E, KV8>;
   err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (err != cudaSuccess) return err;
   err = cudaFuncSetAttribute(kern, cudaFuncAttributePreferredSharedMemoryCarveout, 100);
@@ -1324,8 +1263,6 @@ static cudaError_t launch_typed(const AttnLaunch &a, const WorkspaceLayout &w, c
     tp.num_seqs = a.num_seqs;
     tp.total_q = a.total_q;
     tp.max_tiles = w.max_tiles;
-    tp.k_scales = a.k_scales;
-    tp.v_scales = a.v_scales;
     tp.status = a.status;
     // value cache in whole-block boxes for the tile kernel (block_size rows)
     CUtensorMap vmapb = vmap;
@@ -1333,7 +1270,7 @@ static cudaError_t launch_typed(const AttnLaunch &a, const WorkspaceLayout &w, c
         !encode_block_map(&vmapb, a.value_cache, a.num_blocks, a.num_kv_heads, a.block_size, a.block_size, a.dtype))
       return cudaErrorInvalidValue;
     if (a.tile_start) cudaEventRecord(a.tile_start, stream);
-    err = launch_prefill_tiles<D, G, E, KV8, BSC>(kmap, vmap, vmapb, tp, a.sm_count, stream);
+    err = launch_prefill_tiles<D, G, E, KV8>(kmap, vmap, vmapb, tp, a.sm_count, stream);
     if (err == cudaSuccess && a.tile_stop) cudaEventRecord(a.tile_stop, stream);
     if (err != cudaSuccess) return err;
     ++*launched;
@@ -1367,16 +1304,13 @@ cudaError_t launch_attention(const AttnLaunch &a, cudaStream_t stream, int *laun
   if (!workspace_layout(a.num_seqs, a.total_q, a.max_seq_len, a.num_heads, a.num_kv_heads, a.head_dim, a.kv_fp8, w))
     return cudaErrorInvalidValue;
   const int G = a.num_heads / a.num_kv_heads;
-#define PA_DISPATCH(DD, GG)                                                                            \
-  if (a.head_dim == DD && G == GG) {                                                                   \
-    if (a.k_scales)                                                                                    \
-      return a.dtype == PA_FP16 ? launch_typed<DD, GG, ElemFp16, true, true>(a, w, stream, launched)   \
-                                : launch_typed<DD, GG, ElemBf16, true, true>(a, w, stream, launched);  \
-    if (a.kv_fp8)                                                                                      \
-      return a.dtype == PA_FP16 ? launch_typed<DD, GG, ElemFp16, true, false>(a, w, stream, launched)  \
-                                : launch_typed<DD, GG, ElemBf16, true, false>(a, w, stream, launched); \
-    return a.dtype == PA_FP16 ? launch_typed<DD, GG, ElemFp16, false, false>(a, w, stream, launched)   \
-                              : launch_typed<DD, GG, ElemBf16, false, false>(a, w, stream, launched);  \
+#define PA_DISPATCH(DD, GG)                                                                     \
+  if (a.head_dim == DD && G == GG) {                                                            \
+    if (a.kv_fp8)                                                                               \
+      return a.dtype == PA_FP16 ? launch_typed<DD, GG, ElemFp16, true>(a, w, stream, launched)  \
+                                : launch_typed<DD, GG, ElemBf16, true>(a, w, stream, launched); \
+    return a.dtype == PA_FP16 ? launch_typed<DD, GG, ElemFp16, false>(a, w, stream, launched)   \
+                              : launch_typed<DD, GG, ElemBf16, false>(a, w, stream, launched);  \
   }
   PA_DISPATCH(128, 1) PA_DISPATCH(128, 2) PA_DISPATCH(128, 4) PA_DISPATCH(128, 8)
   PA_DISPATCH(64, 1) PA_DISPATCH(64, 2) PA_DISPATCH(64, 4) PA_DISPATCH(64, 8)
