@@ -545,10 +545,8 @@ pa_status pa_reshape_and_cache_fp8_block(const void *key, const void *value, int
   if (num_seqs == 0 || total_q_tokens == 0) return PA_OK;
   if (max_query_len == 0 || max_query_len > total_q_tokens || max_blocks_per_seq == 0 || num_blocks == 0)
     return PA_ERR_DIMS;
-  // one warp per (unit, KV head, K or V), eight to a CTA of a 31-bit grid
-  const int64_t units = total_q_tokens / block_size + 2 * static_cast<int64_t>(num_seqs);
-  if (units > INT32_MAX || units > (static_cast<int64_t>(INT32_MAX) - 1) * 8 / (2 * static_cast<int64_t>(num_kv_heads)))
-    return PA_ERR_UNSUPPORTED;
+  // units of the launch: a 31-bit grid
+  if (total_q_tokens / block_size + 2 * static_cast<int64_t>(num_seqs) > INT32_MAX) return PA_ERR_UNSUPPORTED;
   if (!key || !value || !key_cache || !value_cache || !k_scales || !v_scales || !block_tables || !seq_lens ||
       !query_start_loc)
     return PA_ERR_NULL;

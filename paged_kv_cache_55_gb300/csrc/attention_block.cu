@@ -15,16 +15,31 @@
 // Every warp is an independent pipeline (own TMA ring, no CTA barrier), takes
 // units from a queue, and computes S^T[16 keys x 8 columns] = K Q^T and
 // O^T += V^T P^T with m16n8k16 fp16 products, codes widened exactly in
-// registers. What it does per tile was cut to what the 32 keys need:
+// registers, one fp16 P' per key (11 bits: a weight moves by at most 2^-11 of
+// itself). What it does per tile was cut to what the 32 keys need:
 //   * the reference m is only moved when a score exceeds it by 2^8 (a warp
 //     vote; P' then stays below 2^8 <= fp16's range), so most tiles reduce no
 //     maximum and rescale nothing;
-//   * one fp16 P' per key (11 bits: a weight moves by at most 2^-11 of itself);
-//   * masks only in a unit's last tiles; K's four codes of a word are used in
-//     the order the widening leaves them (q is loaded to match);
+//   * masks only in a unit's last tiles;
+//   * K's four codes of a word are used in the order the widening leaves them
+//     (q is loaded to match); the transposing 8-bit ldmatrix leaves four keys
+//     of one d in a word of V; the rows of S and the keys of P V are permuted
+//     (s_key, v_key below) so that P needs no further shuffle, eight rows of a
+//     shared-memory phase never meet in a bank, and all keys of a lane in a
+//     half tile share one 8-key scale group;
 //   * block-table entries are loaded one tile ahead, the boxes of a tile are
 //     issued by as many lanes, and its scales travel with it by cp.async on
 //     the same mbarrier.
+// Measured (256 requests, 32 / 8 heads of 128, 958 MB): 167 us under a
+// counter, 5.8 TB/s; the same kernel with the products taken out takes 153 us,
+// so what is left is the loads' own rate (2 KB boxes of 128-byte rows: 6.3
+// TB/s) and the end of the step, where warps finish unevenly. Tried and not
+// kept: K as E4M3 products of a q split into E4M3 terms (no widening; 5 %
+// slower at 256 requests, the same at 8 x 32768), 16-byte cp.async in place of
+// TMA (2-4 % slower), units that shrink towards the end of the queue (17 %
+// slower: a unit's start and its partial cost more than the tail), 8, 10 and
+// 14 warps per SM (2-7 % slower), loading the next unit's record and table
+// entries several tiles ahead (no difference).
 // The planner sizes units from the step's actual lengths, so that a single
 // short request still spreads over the GPU and long ones end together.
 #include <cuda.h>
@@ -54,16 +69,24 @@ constexpr int block_warps(int head_dim) { return head_dim == 256 ? 6 : 12; }
 // so that the sizing calls need no device query.
 constexpr int64_t unit_warps(int head_dim) { return 152 * block_warps(head_dim); }
 
-// Unit size in tiles for `total` tiles (over all KV heads): one unit per warp
-// while that is at most kMinUnit tiles, else up to kUnitsPerWarp units per
-// warp of at least kMinUnit tiles (the queue then evens out requests of
-// different lengths).
-constexpr int kUnitsPerWarp = 3, kMinUnit = 8;
-__host__ __device__ inline int64_t unit_tiles(int64_t total, int64_t warps) {
-  const int64_t one = (total + warps - 1) / warps;
-  int64_t u = (one + kUnitsPerWarp - 1) / kUnitsPerWarp;
-  const int64_t low = one < kMinUnit ? one : kMinUnit;
-  u = u < low ? low : u;
+// Unit size in tiles for `total` tiles (over all KV heads) of `pairs` (request,
+// KV head) pairs. A pair has at most one unit that is not full, so units of
+// total / (warps - pairs) tiles number at most `warps`: one wave, as long as
+// the longest unit. While pairs are few (at most an eighth of the warps) that
+// is within 15 % of an even share, and the fewest partials. With many pairs
+// the shorter requests leave uneven units anyway: then up to kUnitsPerWarp
+// units per warp, of at least kMinUnit tiles, which the queue evens out.
+constexpr int kUnitsPerWarp = 6, kMinUnit = 8;
+__host__ __device__ inline int64_t unit_tiles(int64_t total, int64_t pairs, int64_t warps) {
+  int64_t u;
+  if (pairs * 8 <= warps) {
+    u = (total + warps - pairs - 1) / (warps - pairs);
+  } else {
+    const int64_t one = (total + warps - 1) / warps;
+    const int64_t low = one < kMinUnit ? one : kMinUnit;
+    u = (one + kUnitsPerWarp - 1) / kUnitsPerWarp;
+    u = u < low ? low : u;
+  }
   return u < 1 ? 1 : u;
 }
 
@@ -201,13 +224,14 @@ __global__ void __launch_bounds__(NT) block_plan_kernel(const PlanParams p) {
   griddep_launch_dependents();
   const bool once = p.num_seqs <= NT;
   Request r{};
-  unsigned long long mine = 0, total;
+  unsigned long long mine = 0, total;  // key tiles, and decode requests in the top 24 bits
   for (int b = tid; b < p.num_seqs; b += NT) {
     r = read_request(p, b, true);
-    mine += r.key_tiles;
+    mine += static_cast<unsigned long long>(r.key_tiles) | (r.key_tiles > 0 ? 1ull << 40 : 0);
   }
   block_scan<NT>(mine, warp_tot, &total);
-  const int64_t U64 = unit_tiles(static_cast<int64_t>(total) * p.num_kv_heads, p.warps);
+  const int64_t U64 = unit_tiles(static_cast<int64_t>(total & ((1ull << 40) - 1)) * p.num_kv_heads,
+                                 static_cast<int64_t>(total >> 40) * p.num_kv_heads, p.warps);
   const int U = U64 > (1 << 24) ? (1 << 24) : static_cast<int>(U64);
   const int unit_keys = U * kTile;
   mine = 0;
@@ -316,14 +340,25 @@ __device__ __forceinline__ void cp_async_4(uint32_t dst, const void *src, int sr
 __device__ __forceinline__ void cp_async_mbar_arrive(uint32_t bar) {
   asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];\n" ::"r"(bar) : "memory");
 }
-__device__ __forceinline__ float4 ld_shared4(uint32_t addr) {
-  float4 v;
-  asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];\n"
-               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
-               : "r"(addr)
-               : "memory");
+__device__ __forceinline__ float ld_shared(uint32_t addr) {
+  float v;
+  asm volatile("ld.shared.f32 %0, [%1];\n" : "=f"(v) : "r"(addr) : "memory");
   return v;
 }
+// Two 16 x 16 byte matrices, transposed: matrix i's row r at the address lane
+// 16 i + r gives; lane l receives rows 4 (l % 4) .. + 3 of columns l / 4 (r0)
+// and l / 4 + 8 (r1) of matrix 0, and the same of matrix 1 in r2, r3.
+__device__ __forceinline__ void ldsm_b8_x2_t(uint32_t addr, uint32_t &r0, uint32_t &r1, uint32_t &r2, uint32_t &r3) {
+  asm volatile("ldmatrix.sync.aligned.m16n16.x2.trans.shared.b8 {%0, %1, %2, %3}, [%4];\n"
+               : "=r"(r0), "=r"(r1), "=r"(r2), "=r"(r3)
+               : "r"(addr));
+}
+// Key of a 16-key half that row r of S holds: 0-3, 12-15, 4-7, 8-11. P of rows
+// 2t, 2t + 1 and 2t + 8, 2t + 9 (one lane's after the transposition) multiplies
+// the four keys that lane's V words hold, so V's row i is key
+// s_key(2 (i / 4) + i % 2 + 8 (i / 2 % 2)).
+__device__ __forceinline__ int s_key(int r) { return r < 4 ? r : (r < 8 ? r + 8 : r - 4); }
+__device__ __forceinline__ int v_key(int i) { return s_key(2 * (i >> 2) + (i & 1) + 8 * ((i >> 1) & 1)); }
 // Four codes -> fp16 pairs (c0, c1) and (c2, c3), exactly.
 __device__ __forceinline__ void widen_pairs(uint32_t w, uint32_t &p01, uint32_t &p23) {
   asm("{\n .reg .b16 l, h;\n mov.b32 {l, h}, %2;\n cvt.rn.f16x2.e4m3x2 %0, l;\n cvt.rn.f16x2.e4m3x2 %1, h;\n}\n"
@@ -344,8 +379,8 @@ __global__ void __launch_bounds__(NWARPS * 32, 1)
   constexpr int S = kRingBytes / (NWARPS * T::SLOT_BYTES);  // ring slots per warp
   static_assert(S >= 2, "ring needs at least two slots");
   constexpr int MT = D / 16;
-  // an ldmatrix.x4 covers 32 d, so fragments come in pairs (head_dim 80: one more, all zero)
-  constexpr int MQ = 2 * ((D + 31) / 32);
+  constexpr int DK = (D + 31) / 32;  // 32-d steps (head_dim 80: the last 16 d are zero)
+  constexpr int MQ = 2 * DK;         // 16-d rows of O
   constexpr unsigned FULL = 0xffffffffu;
 
   extern __shared__ unsigned char smem_raw[];
@@ -401,11 +436,14 @@ __global__ void __launch_bounds__(NWARPS * 32, 1)
     U.kb1 = (U.kv_end + kTile - 1) / kTile;
     return U;
   };
-  auto next_unit = [&]() {
-    int u = 0;
-    if (lane == 0) u = atomicAdd(p.counts + 1, 1);
-    return read_unit(__shfl_sync(FULL, u, 0));
+  // Tickets of the queue are drawn a unit ahead: the atomic's answer is first
+  // looked at when the next unit's tiles are to be issued.
+  const bool queue = total_units > static_cast<int>(gridDim.x) * NWARPS;
+  int ticket = total_units;
+  auto draw = [&]() {
+    if (queue && lane == 0) ticket = atomicAdd(p.counts + 1, 1);
   };
+  auto next_unit = [&]() { return read_unit(queue ? __shfl_sync(FULL, ticket, 0) : total_units); };
   // block-table entry of box `lane` of tile kb (negative: no box)
   auto table_entry = [&](const Unit &U, int kb) {
     const int key = kb * kTile + lane * box_rows;
@@ -417,6 +455,7 @@ __global__ void __launch_bounds__(NWARPS * 32, 1)
   // Units are taken in order: `cur` is computed, the producer may be one unit
   // ahead in `nxt`. phys: table entries of the tile it issues next.
   Unit cur = read_unit(blockIdx.x + warp * gridDim.x);  // the first without the queue
+  if (cur.valid) draw();
   Unit nxt;
   nxt.valid = 0;
   bool have_nxt = false, on_nxt = false;
@@ -458,10 +497,8 @@ __global__ void __launch_bounds__(NWARPS * 32, 1)
   auto produce = [&](uint32_t limit) {
     while (issued < limit) {
       if (!on_nxt && p_kb >= cur.kb1) {
-        if (!have_nxt) {
-          nxt = next_unit();
-          have_nxt = true;
-        }
+        nxt = next_unit();
+        have_nxt = true;
         on_nxt = true;
         p_kb = nxt.kb0;
         phys = nxt.kb0 < nxt.kb1 ? table_entry(nxt, nxt.kb0) : -1;
@@ -474,7 +511,10 @@ __global__ void __launch_bounds__(NWARPS * 32, 1)
     }
   };
 
-  const int arow = (lane & 7) + ((lane >> 3) & 1) * 8;  // ldmatrix row of K and V
+  // ldmatrix rows of a half tile: K's (S rows lane % 16), V's (V rows lane % 16)
+  const int krow = s_key(lane & 15), vrow = v_key(lane & 15);
+  const int grp = lane >> 4;                           // 8-key scale group of the lane's keys within a half
+  const int key_a = s_key(lane >> 2), key_b = s_key((lane >> 2) + 8);  // the lane's two keys of a half
 
   while (cur.valid) {
     // ---- q fragments (B operand of S^T = K Q^T): k step kk pairs d = 16 kk + 4 (lane % 4) + (0, 1) and (2, 3) ----
@@ -556,20 +596,23 @@ __global__ void __launch_bounds__(NWARPS * 32, 1)
         fence_proxy_async_smem();  // before the slot's next TMA fill
         __syncwarp();
       }
-      // scores: keys lane / 4 + 8 i (i = 0..3) in s[i / 2][2 (i % 2) + column]
+      // scores of half h: keys key_a (columns 0, 1) and key_b (2, 3)
       float s[2][4];
       {
-        float sa[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
-        float sb[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
+        float sb[2][4];
 #pragma unroll
-        for (int j = 0; j < MQ / 2; ++j) {
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) s[h][i] = sb[h][i] = 0.f;
+#pragma unroll
+        for (int j = 0; j < DK; ++j) {
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
             uint32_t r0, r1, r2, r3, a0, a1, a2, a3;
-            ldsm_x4(kt + h * 16 * T::ROW + T::off(arow, 2 * j + (lane >> 4)), r0, r1, r2, r3);
+            ldsm_x4(kt + h * 16 * T::ROW + T::off(krow, 2 * j + (lane >> 4)), r0, r1, r2, r3);
             widen_pairs(r0, a0, a2);
             widen_pairs(r1, a1, a3);
-            M::mma(sa[h], a0, a1, a2, a3, qf[2 * j][0], qf[2 * j][1]);
+            M::mma(s[h], a0, a1, a2, a3, qf[2 * j][0], qf[2 * j][1]);
             widen_pairs(r2, a0, a2);
             widen_pairs(r3, a1, a3);
             M::mma(sb[h], a0, a1, a2, a3, qf[2 * j + 1][0], qf[2 * j + 1][1]);
@@ -578,30 +621,30 @@ __global__ void __launch_bounds__(NWARPS * 32, 1)
 #pragma unroll
         for (int h = 0; h < 2; ++h)
 #pragma unroll
-          for (int i = 0; i < 4; ++i) s[h][i] = sa[h][i] + sb[h][i];
+          for (int i = 0; i < 4; ++i) s[h][i] += sb[h][i];
       }
-      const float4 k4 = ld_shared4(smem_u32(&scales[warp][slot][0]));
-      const float4 v4 = ld_shared4(smem_u32(&scales[warp][slot][4]));
-      const float gk[4] = {k4.x, k4.y, k4.z, k4.w}, gv[4] = {v4.x, v4.y, v4.z, v4.w};
+      const uint32_t sc = smem_u32(&scales[warp][slot][grp]);
+      const float gk[2] = {ld_shared(sc), ld_shared(sc + 8)}, gv[2] = {ld_shared(sc + 16), ld_shared(sc + 24)};
       if (key0 + kTile > all_see) {  // a unit's last tiles: keys some column does not see
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
+        for (int h = 0; h < 2; ++h)
 #pragma unroll
-          for (int c = 0; c < 2; ++c)
-            if (key0 + 8 * i + (lane >> 2) >= lim[c]) s[i >> 1][2 * (i & 1) + c] = -INFINITY;
+          for (int i = 0; i < 4; ++i)
+            if (key0 + 16 * h + (i < 2 ? key_a : key_b) >= lim[i & 1]) s[h][i] = -INFINITY;
       }
-      float e[4][2], glv[4];
+      // exponents against the references; a group past the last key has scales
+      // 0 and its (masked) scores stay -inf
+      float e[2][4], factor[2][2], glv[2];
       float top = -INFINITY;
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        glv[i] = __log2f(gv[i]);
+      for (int h = 0; h < 2; ++h) {
+        glv[h] = __log2f(gv[h]);
 #pragma unroll
-        for (int c = 0; c < 2; ++c) {
-          // a group past the last key has scales 0: its (masked) scores stay -inf
-          const float f = gk[i] > 0.f ? col_scale[c] * gk[i] : 1.f;
-          const float x = s[i >> 1][2 * (i & 1) + c];
-          e[i][c] = fmaf(x, f, glv[i] - m[c]);
-          top = fmaxf(top, e[i][c]);
+        for (int c = 0; c < 2; ++c) factor[h][c] = gk[h] > 0.f ? col_scale[c] * gk[h] : 1.f;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          e[h][i] = fmaf(s[h][i], factor[h][i & 1], glv[h] - m[i & 1]);
+          top = fmaxf(top, e[h][i]);
         }
       }
       if (__any_sync(FULL, top > kGrowLog2)) {
@@ -610,11 +653,12 @@ __global__ void __launch_bounds__(NWARPS * 32, 1)
         for (int c = 0; c < 2; ++c) {
           float mx = -INFINITY;
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const float f = gk[i] > 0.f ? col_scale[c] * gk[i] : 1.f;
-            e[i][c] = __fadd_rn(__fmul_rn(s[i >> 1][2 * (i & 1) + c], f), glv[i]);
-            mx = fmaxf(mx, e[i][c]);
-          }
+          for (int h = 0; h < 2; ++h)
+#pragma unroll
+            for (int i = c; i < 4; i += 2) {
+              e[h][i] = __fadd_rn(__fmul_rn(s[h][i], factor[h][c]), glv[h]);
+              mx = fmaxf(mx, e[h][i]);
+            }
 #pragma unroll
           for (int off = 4; off < 32; off <<= 1) mx = fmaxf(mx, __shfl_xor_sync(FULL, mx, off));
           const float mn = fmaxf(m[c], mx);
@@ -627,31 +671,35 @@ __global__ void __launch_bounds__(NWARPS * 32, 1)
             o[mt][2 + c] *= al;
           }
 #pragma unroll
-          for (int i = 0; i < 4; ++i) e[i][c] = __fsub_rn(e[i][c], mn);
+          for (int h = 0; h < 2; ++h)
+#pragma unroll
+            for (int i = c; i < 4; i += 2) e[h][i] = __fsub_rn(e[h][i], mn);
         }
       }
-      uint32_t pk[4];
+      uint32_t pk[2][2];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const float inv = gv[i] > 0.f ? __fdividef(1.f, gv[i]) : 0.f;
-        const float p0 = ex2_approx(e[i][0]), p1 = ex2_approx(e[i][1]);
-        l[0] = fmaf(p0, inv, l[0]);
-        l[1] = fmaf(p1, inv, l[1]);
-        pk[i] = movmatrix_t(M::pack(p0, p1));
+      for (int h = 0; h < 2; ++h) {
+        const float inv = gv[h] > 0.f ? __fdividef(1.f, gv[h]) : 0.f;
+        const float p0 = ex2_approx(e[h][0]), p1 = ex2_approx(e[h][1]);
+        const float p2 = ex2_approx(e[h][2]), p3 = ex2_approx(e[h][3]);
+        l[0] = fmaf(p0 + p2, inv, l[0]);
+        l[1] = fmaf(p1 + p3, inv, l[1]);
+        pk[h][0] = movmatrix_t(M::pack(p0, p1));
+        pk[h][1] = movmatrix_t(M::pack(p2, p3));
       }
-      // O^T += V^T P^T: row lane / 4 of m tile mt holds d = 16 mt + 2 (lane / 4), row lane / 4 + 8 the next one
+      // O^T += V^T P^T: rows lane / 4 and lane / 4 + 8 of m tile mt are d = 16 mt + those
 #pragma unroll
-      for (int j = 0; j < MQ / 2; ++j) {
+      for (int j = 0; j < DK; ++j) {
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-          uint32_t r0, r1, r2, r3, l0, h0, l1, h1;
-          ldsm_x4_t(vt + h * 16 * T::ROW + T::off(arow, 2 * j + (lane >> 4)), r0, r1, r2, r3);
-          M::from_e4m3x4(r0, l0, h0);
-          M::from_e4m3x4(r1, l1, h1);
-          M::mma(o[2 * j], l0, h0, l1, h1, pk[2 * h], pk[2 * h + 1]);
-          M::from_e4m3x4(r2, l0, h0);
-          M::from_e4m3x4(r3, l1, h1);
-          M::mma(o[2 * j + 1], l0, h0, l1, h1, pk[2 * h], pk[2 * h + 1]);
+          uint32_t r0, r1, r2, r3, a0, a1, a2, a3;
+          ldsm_b8_x2_t(vt + h * 16 * T::ROW + T::off(vrow, 2 * j + (lane >> 4)), r0, r1, r2, r3);
+          widen_pairs(r0, a0, a2);
+          widen_pairs(r1, a1, a3);
+          M::mma(o[2 * j], a0, a1, a2, a3, pk[h][0], pk[h][1]);
+          widen_pairs(r2, a0, a2);
+          widen_pairs(r3, a1, a3);
+          M::mma(o[2 * j + 1], a0, a1, a2, a3, pk[h][0], pk[h][1]);
         }
       }
       __syncwarp();  // every lane is done with the slot before it is refilled
@@ -673,12 +721,13 @@ __global__ void __launch_bounds__(NWARPS * 32, 1)
                     static_cast<int64_t>(cur.kvh * G + g) * D;
 #pragma unroll
         for (int mt = 0; mt < MT; ++mt) {
-          // transposed, lo8 holds d = 16 mt + 4 (lane % 4) + (0, 2) of one column, hi8 (1, 3)
+          // transposed: lo8 holds d = 16 mt + 2 (lane % 4) + (0, 1) of one column, hi8 those + 8
           const uint32_t lo8 = movmatrix_t(E::pack(o[mt][0] * inv0, o[mt][1] * inv1));
           const uint32_t hi8 = movmatrix_t(E::pack(o[mt][2] * inv0, o[mt][3] * inv1));
-          if (qi < cur.nrows)
-            *reinterpret_cast<uint2 *>(dst + 16 * mt + 4 * (lane & 3)) =
-                make_uint2(__byte_perm(lo8, hi8, 0x5410), __byte_perm(lo8, hi8, 0x7632));
+          if (qi < cur.nrows) {
+            *reinterpret_cast<uint32_t *>(dst + 16 * mt + 2 * (lane & 3)) = lo8;
+            *reinterpret_cast<uint32_t *>(dst + 16 * mt + 2 * (lane & 3) + 8) = hi8;
+          }
         }
       } else {
         const int64_t base = (static_cast<int64_t>(cur.item) * Hkv + cur.kvh) * kCols;
@@ -687,10 +736,12 @@ __global__ void __launch_bounds__(NWARPS * 32, 1)
           const int col = 2 * (lane & 3) + c;
           if (col / G < cur.nrows) {
             const float inv = c ? inv1 : inv0;
-            float *dst = p.part_o + (base + col) * D + 2 * (lane >> 2);
+            float *dst = p.part_o + (base + col) * D + (lane >> 2);
 #pragma unroll
-            for (int mt = 0; mt < MT; ++mt)
-              *reinterpret_cast<float2 *>(dst + 16 * mt) = make_float2(o[mt][c] * inv, o[mt][2 + c] * inv);
+            for (int mt = 0; mt < MT; ++mt) {
+              dst[16 * mt] = o[mt][c] * inv;
+              dst[16 * mt + 8] = o[mt][2 + c] * inv;
+            }
             if (lane < 4) p.part_lse[base + col] = l[c] > 0.f ? m[c] + __log2f(l[c]) : -INFINITY;
           }
         }
@@ -705,21 +756,24 @@ __global__ void __launch_bounds__(NWARPS * 32, 1)
     }
     cur = nxt;
     have_nxt = on_nxt = false;
+    if (cur.valid) draw();
   }
 }
 
 // ---- merge -----------------------------------------------------------------
 
-// One CTA of eight warps per (request, KV head): the used columns (query rows
-// x G, at most 8) rounded up to a power of two NC take a warp each, and the
-// 8 / NC warps of a column share its partitions in contiguous runs, joined
-// through shared memory in order (the same bits every time). A warp reads
-// eight partitions at a time with a running maximum of their log-sum-exps.
-template <int D, int G, typename E>
-__global__ void __launch_bounds__(256) block_merge_kernel(const MergeParams p) {
+// One CTA of NW warps per (request, KV head): the used columns (query rows x
+// G, at most 8) rounded up to a power of two NC take a warp each, NW / NC warps
+// of a column share its partitions in contiguous runs, joined through shared
+// memory in order (the same bits every time), or (NC > NW) a warp takes several
+// columns. A warp reads eight partitions at a time with a running maximum of
+// their log-sum-exps. Sixteen warps when the pairs are few (their partitions
+// are then many), four when there are several CTAs per SM anyway.
+template <int D, int G, typename E, int NW>
+__global__ void __launch_bounds__(NW * 32) block_merge_kernel(const MergeParams p) {
   constexpr int EPL = (D + 31) / 32;  // outputs per lane (head_dim 80, 96: the last lanes' unused)
   constexpr bool VEC4 = D % 128 == 0, VEC2 = D == 64;
-  __shared__ float s_m[kCols], s_w[kCols], s_acc[kCols][32 * EPL];
+  __shared__ float s_m[NW], s_w[NW], s_acc[NW][32 * EPL];
   griddep_wait();
   griddep_launch_dependents();
   const int b = blockIdx.x / p.num_kv_heads, kvh = blockIdx.x - b * p.num_kv_heads;
@@ -729,92 +783,96 @@ __global__ void __launch_bounds__(256) block_merge_kernel(const MergeParams p) {
   if (np <= 1 || ql < 1 || ql * G > kCols) return;
   const int cols = ql * G;
   const int nc = cols <= 1 ? 1 : (cols <= 2 ? 2 : (cols <= 4 ? 4 : 8));
-  const int col = warp % nc, sub = warp / nc, subs = kCols / nc;
+  const int wc = nc < NW ? nc : NW;  // columns in parallel
+  const int sub = warp / wc, subs = NW / wc;
   const int k_begin = np * sub / subs, k_end = np * (sub + 1) / subs;
-  float M = -INFINITY, wsum = 0.f, acc[EPL];
+  for (int col0 = 0; col0 < cols; col0 += wc) {
+    const int col = col0 + warp % wc;
+    float M = -INFINITY, wsum = 0.f, acc[EPL];
 #pragma unroll
-  for (int e = 0; e < EPL; ++e) acc[e] = 0.f;
-  if (col < cols) {
-    for (int k0 = k_begin; k0 < k_end; k0 += 8) {
-      float lv[8], ov[8][EPL];
+    for (int e = 0; e < EPL; ++e) acc[e] = 0.f;
+    if (col < cols) {
+      for (int k0 = k_begin; k0 < k_end; k0 += 8) {
+        float lv[8], ov[8][EPL];
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const int k = min(k0 + j, k_end - 1);
-        const int item = min(max(k == np - 1 && rest >= 0 ? rest : full0 + k, 0), p.max_items - 1);
-        const int64_t at = (static_cast<int64_t>(item) * p.num_kv_heads + kvh) * kCols + col;
-        lv[j] = ld_cg(p.part_lse + at);
-        const float *src = p.part_o + at * D + lane * EPL;
-        if constexpr (VEC2) {
-          const float2 v = ld_cg(reinterpret_cast<const float2 *>(src));
-          ov[j][0] = v.x, ov[j][1] = v.y;
-        } else if constexpr (VEC4) {
+        for (int j = 0; j < 8; ++j) {
+          const int k = min(k0 + j, k_end - 1);
+          const int item = min(max(k == np - 1 && rest >= 0 ? rest : full0 + k, 0), p.max_items - 1);
+          const int64_t at = (static_cast<int64_t>(item) * p.num_kv_heads + kvh) * kCols + col;
+          lv[j] = ld_cg(p.part_lse + at);
+          const float *src = p.part_o + at * D + lane * EPL;
+          if constexpr (VEC2) {
+            const float2 v = ld_cg(reinterpret_cast<const float2 *>(src));
+            ov[j][0] = v.x, ov[j][1] = v.y;
+          } else if constexpr (VEC4) {
 #pragma unroll
-          for (int e = 0; e < EPL; e += 4) {
-            const float4 v = ld_cg(reinterpret_cast<const float4 *>(src + e));
-            ov[j][e] = v.x, ov[j][e + 1] = v.y, ov[j][e + 2] = v.z, ov[j][e + 3] = v.w;
+            for (int e = 0; e < EPL; e += 4) {
+              const float4 v = ld_cg(reinterpret_cast<const float4 *>(src + e));
+              ov[j][e] = v.x, ov[j][e + 1] = v.y, ov[j][e + 2] = v.z, ov[j][e + 3] = v.w;
+            }
+          } else {
+#pragma unroll
+            for (int e = 0; e < EPL; ++e) ov[j][e] = lane * EPL + e < D ? ld_cg(src + e) : 0.f;
           }
-        } else {
-#pragma unroll
-          for (int e = 0; e < EPL; ++e) ov[j][e] = lane * EPL + e < D ? ld_cg(src + e) : 0.f;
         }
-      }
-      float Mn = M;
+        float Mn = M;
 #pragma unroll
-      for (int j = 0; j < 8; ++j)
-        if (k0 + j < k_end) Mn = fmaxf(Mn, lv[j]);
-      const float Ms = Mn == -INFINITY ? 0.f : Mn;
-      const float r = ex2_approx(M - Ms);
-      wsum *= r;
+        for (int j = 0; j < 8; ++j)
+          if (k0 + j < k_end) Mn = fmaxf(Mn, lv[j]);
+        const float Ms = Mn == -INFINITY ? 0.f : Mn;
+        const float r = ex2_approx(M - Ms);
+        wsum *= r;
 #pragma unroll
-      for (int e = 0; e < EPL; ++e) acc[e] *= r;
-      M = Mn;
+        for (int e = 0; e < EPL; ++e) acc[e] *= r;
+        M = Mn;
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        if (k0 + j < k_end) {
-          const float w = ex2_approx(lv[j] - Ms);
-          wsum += w;
+        for (int j = 0; j < 8; ++j) {
+          if (k0 + j < k_end) {
+            const float w = ex2_approx(lv[j] - Ms);
+            wsum += w;
 #pragma unroll
-          for (int e = 0; e < EPL; ++e) acc[e] += w * ov[j][e];
+            for (int e = 0; e < EPL; ++e) acc[e] += w * ov[j][e];
+          }
         }
       }
     }
-  }
-  if (subs > 1) {
-    if (lane == 0) {
-      s_m[warp] = M;
-      s_w[warp] = wsum;
+    if (subs > 1) {  // then one round of columns
+      if (lane == 0) {
+        s_m[warp] = M;
+        s_w[warp] = wsum;
+      }
+#pragma unroll
+      for (int e = 0; e < EPL; ++e) s_acc[warp][e * 32 + lane] = acc[e];
+      __syncthreads();
+      if (sub > 0) return;
+      for (int k = 1; k < subs; ++k) {
+        const int w = k * wc + warp;
+        const float Mo = s_m[w], Mn = fmaxf(M, Mo), Ms = Mn == -INFINITY ? 0.f : Mn;
+        const float ra = ex2_approx(M - Ms), rb = ex2_approx(Mo - Ms);
+        wsum = wsum * ra + s_w[w] * rb;
+#pragma unroll
+        for (int e = 0; e < EPL; ++e) acc[e] = acc[e] * ra + s_acc[w][e * 32 + lane] * rb;
+        M = Mn;
+      }
     }
+    if (col >= cols) continue;
+    const float inv = wsum > 0.f ? 1.f / wsum : 0.f;
+    bf16 *dst = p.out + static_cast<int64_t>(q0 + col / G) * p.num_heads * D +
+                static_cast<int64_t>(kvh * G + col % G) * D + lane * EPL;
+    if constexpr (VEC2) {
+      *reinterpret_cast<uint32_t *>(dst) = E::pack(acc[0] * inv, acc[1] * inv);
+    } else if constexpr (VEC4) {
 #pragma unroll
-    for (int e = 0; e < EPL; ++e) s_acc[warp][e * 32 + lane] = acc[e];
-    __syncthreads();
-    if (sub > 0) return;
-    for (int k = 1; k < subs; ++k) {
-      const int w = k * nc + col;
-      const float Mo = s_m[w], Mn = fmaxf(M, Mo), Ms = Mn == -INFINITY ? 0.f : Mn;
-      const float ra = ex2_approx(M - Ms), rb = ex2_approx(Mo - Ms);
-      wsum = wsum * ra + s_w[w] * rb;
+      for (int e = 0; e < EPL; e += 4)
+        *reinterpret_cast<uint2 *>(dst + e) =
+            make_uint2(E::pack(acc[e] * inv, acc[e + 1] * inv), E::pack(acc[e + 2] * inv, acc[e + 3] * inv));
+    } else {
 #pragma unroll
-      for (int e = 0; e < EPL; ++e) acc[e] = acc[e] * ra + s_acc[w][e * 32 + lane] * rb;
-      M = Mn;
+      for (int e = 0; e < EPL; ++e)
+        if (lane * EPL + e < D)
+          *reinterpret_cast<unsigned short *>(dst + e) =
+              static_cast<unsigned short>(E::pack(acc[e] * inv, 0.f) & 0xffffu);
     }
-  }
-  if (col >= cols) return;
-  const float inv = wsum > 0.f ? 1.f / wsum : 0.f;
-  bf16 *dst = p.out + static_cast<int64_t>(q0 + col / G) * p.num_heads * D +
-              static_cast<int64_t>(kvh * G + col % G) * D + lane * EPL;
-  if constexpr (VEC2) {
-    *reinterpret_cast<uint32_t *>(dst) = E::pack(acc[0] * inv, acc[1] * inv);
-  } else if constexpr (VEC4) {
-#pragma unroll
-    for (int e = 0; e < EPL; e += 4)
-      *reinterpret_cast<uint2 *>(dst + e) =
-          make_uint2(E::pack(acc[e] * inv, acc[e + 1] * inv), E::pack(acc[e + 2] * inv, acc[e + 3] * inv));
-  } else {
-#pragma unroll
-    for (int e = 0; e < EPL; ++e)
-      if (lane * EPL + e < D)
-        *reinterpret_cast<unsigned short *>(dst + e) =
-            static_cast<unsigned short>(E::pack(acc[e] * inv, 0.f) & 0xffffu);
   }
 }
 
@@ -972,8 +1030,11 @@ cudaError_t launch_typed(const AttnLaunch &a, const BlockWorkspace &w, cudaStrea
     mp.part_o = dp.part_o;
     mp.part_lse = dp.part_lse;
     mp.out = dp.out;
-    err = launch_pdl(block_merge_kernel<D, G, E>, dim3(static_cast<unsigned>(a.num_seqs * a.num_kv_heads)), dim3(256),
-                     0, stream, mp);
+    const unsigned pairs = static_cast<unsigned>(a.num_seqs * a.num_kv_heads);
+    if (pairs <= 2u * static_cast<unsigned>(a.sm_count))
+      err = launch_pdl(block_merge_kernel<D, G, E, 16>, dim3(pairs), dim3(16 * 32), 0, stream, mp);
+    else
+      err = launch_pdl(block_merge_kernel<D, G, E, 4>, dim3(pairs), dim3(4 * 32), 0, stream, mp);
     if (err != cudaSuccess) return err;
     ++*launched;
   }
@@ -988,7 +1049,8 @@ bool block_workspace_layout(int32_t num_seqs, int32_t total_q, int32_t max_seq_l
       num_heads % num_kv_heads != 0 || num_heads / num_kv_heads > kCols)
     return false;
   const int G = num_heads / num_kv_heads;
-  // a request of t key tiles gives at most t / U + 1 items, U >= total / (kUnitsPerWarp * warps)
+  // a request of t key tiles gives at most t / U + 1 items, U >= total / (kUnitsPerWarp * warps), or
+  // U >= total / warps when pairs are few
   const int64_t key_tiles = (static_cast<int64_t>(max_seq_len) + kTile - 1) / kTile;
   const int64_t full = (kUnitsPerWarp * unit_warps(head_dim) + num_kv_heads - 1) / num_kv_heads;
   int64_t items = static_cast<int64_t>(num_seqs) * key_tiles;

@@ -25,7 +25,7 @@ namespace pa {
 
 namespace {
 
-constexpr int kScatterWarps = 8;
+constexpr int kScatterWarps = 16;  // per CTA, at most
 constexpr int kMinScaleExp = -64;
 
 // Largest finite magnitude of a 16-bit pair, bit pattern per half (magnitudes
@@ -57,50 +57,91 @@ __device__ __forceinline__ uint32_t rescale4(uint32_t w, float ratio) {
   return p0 | (p1 << 16);
 }
 
-// Index of the request that owns unit u: the largest b with start(b) <= u,
-// start(b) = query_start_loc[b] / bs + 2 b. A request of n > 0 rows touches at
-// most n / bs + 2 blocks, so the units [start(b), start(b + 1)) cover them.
-// 32 probes per step.
-__device__ __forceinline__ int find_request(const int32_t *qsl, int num_seqs, int shift, int u, int lane) {
-  int lo = 0, n = num_seqs;  // the answer is in [lo, lo + n)
-  while (n > 1) {
-    const int step = (n + 31) / 32;
-    const int b = lo + lane * step;
-    const bool below = lane * step < n && (ld_cg(qsl + b) >> shift) + 2 * b <= u;
-    const unsigned votes = __ballot_sync(0xffffffffu, below);
-    const int k = votes ? 31 - __clz(votes) : 0;  // start(lo) <= u always holds
-    lo += k * step;
-    n = min(step, n - k * step);
-  }
-  return lo;
+// E4M3 codes of x / scale. A power-of-two scale divides by multiplying with
+// its inverse (exact, the same rounding); any other is divided by.
+template <typename E>
+__device__ __forceinline__ uint2 quantize8_by(uint4 a, float scale, float inverse, bool power_of_two) {
+  if (!power_of_two) return quantize8<E>(a, scale);
+  const uint32_t x[4] = {a.x, a.y, a.z, a.w};
+  uint32_t c[4];
+#pragma unroll
+  for (int k = 0; k < 4; ++k) c[k] = e4m3x2_from_f32(E::lo(x[k]) * inverse, E::hi(x[k]) * inverse);
+  return make_uint2(c[0] | (c[1] << 16), c[2] | (c[3] << 16));
 }
 
+// The request that owns unit u: the largest b with start(b) <= u, where
+// start(b) = query_start_loc[b] / bs + 2 b. A request of n > 0 rows touches at
+// most n / bs + 2 blocks, so the units [start(b), start(b + 1)) cover them.
+// Every thread probes one request per round (one round up to 256 requests).
+// The last round's probes load the request's lengths as well, and the last
+// thread that lies at or below u publishes them: {b, q0, q1, length}.
+__device__ __forceinline__ void find_request(const BlockScatterLaunch &p, int shift, int u, int4 *found) {
+  __shared__ int s_lo;
+  int lo = 0, n = p.num_seqs;  // the answer is in [lo, lo + n)
+  for (;;) {
+    const int step = (n + blockDim.x - 1) / blockDim.x;
+    const int at = static_cast<int>(threadIdx.x) * step;
+    int q0 = 0, q1 = 0, len = 0;
+    bool below = false, last = false;
+    if (at < n) {
+      const int b = lo + at;
+      q0 = ld_cg(p.query_start_loc + b);
+      if (step == 1) {
+        q1 = ld_cg(p.query_start_loc + b + 1);
+        len = ld_cg(p.seq_lens + b);
+      }
+      const int next = min(at + step, n);  // the next probe's request
+      const int qn = next < n ? (step == 1 ? q1 : ld_cg(p.query_start_loc + lo + next)) : 0;
+      below = (q0 >> shift) + 2 * b <= u || at == 0;
+      last = below && (next >= n || (qn >> shift) + 2 * (lo + next) > u);
+    }
+    // (a query_start_loc that is not sorted may elect several threads or none: any one of them is in range)
+    if (threadIdx.x == 0) {
+      s_lo = lo;
+      if (step == 1) *found = make_int4(lo, q0, q1, len);
+    }
+    __syncthreads();
+    if (last) {
+      s_lo = lo + at;
+      if (step == 1) *found = make_int4(lo + at, q0, q1, len);
+    }
+    __syncthreads();
+    if (step == 1) return;
+    const int picked = s_lo;
+    n = min(step, n - (picked - lo));
+    lo = picked;
+    __syncthreads();  // s_lo has been read
+  }
+}
+
+// One CTA per unit (touched block of a request), a warp per (K or V, KV head):
+// a warp loads the block's new rows of its head into registers, reduces their
+// largest magnitude, and stores their codes.
 template <int D, int BS, typename E>
 __global__ void __launch_bounds__(kScatterWarps * 32) block_scatter_kernel(const BlockScatterLaunch p) {
   constexpr int CPR = D / 8;                   // 8-element chunks per row
   constexpr int NV = (BS * CPR + 31) / 32;     // chunks per lane, at most
   constexpr int SHIFT = BS == 8 ? 3 : (BS == 16 ? 4 : 5);
+  __shared__ int4 s_found;
   griddep_wait();
   griddep_launch_dependents();
-  const int lane = threadIdx.x & 31;
-  const int64_t w = static_cast<int64_t>(blockIdx.x) * kScatterWarps + (threadIdx.x >> 5);
-  // warp w: K or V of one KV head of one unit
-  const int per_unit = 2 * p.num_kv_heads;
-  const int64_t u64 = w / per_unit;
-  const int r = static_cast<int>(w - u64 * per_unit);
-  const bool is_v = r >= p.num_kv_heads;
-  const int kvh = is_v ? r - p.num_kv_heads : r;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
+  const int u = blockIdx.x;
   // steps of one-token requests: unit u is request u
   const bool single = p.max_query_len <= 1;
-  const int64_t units = single ? p.num_seqs : (p.total_q >> SHIFT) + 2 * static_cast<int64_t>(p.num_seqs);
-  if (u64 >= units) return;
-  const int u = static_cast<int>(u64);
-  const int b = single ? u : find_request(p.query_start_loc, p.num_seqs, SHIFT, u, lane);
-  const int q0 = ld_cg(p.query_start_loc + b), q1 = ld_cg(p.query_start_loc + b + 1);
-  const int len = ld_cg(p.seq_lens + b);
+  int b, q0, q1, len;
+  if (single) {
+    b = u;
+    q0 = ld_cg(p.query_start_loc + b);
+    q1 = ld_cg(p.query_start_loc + b + 1);
+    len = ld_cg(p.seq_lens + b);
+  } else {
+    find_request(p, SHIFT, u, &s_found);
+    const int4 f = s_found;
+    b = f.x, q0 = f.y, q1 = f.z, len = f.w;
+  }
   const int ql = q1 - q0;
-  const int i = single ? 0 : u - ((q0 >> SHIFT) + 2 * b);  // touched block of the request
-  const bool report = lane == 0 && r == 0;
+  const bool report = threadIdx.x == 0;
   if (q0 < 0 || ql < 0 || q1 > p.total_q || (b == 0 && q0 != 0) || (b == p.num_seqs - 1 && q1 != p.total_q)) {
     if (report) flag_error(p.status, PA_FLAG_QUERY_LOC);
     return;
@@ -110,68 +151,75 @@ __global__ void __launch_bounds__(kScatterWarps * 32) block_scatter_kernel(const
     if (report) flag_error(p.status, PA_FLAG_LENGTHS);
     return;
   }
+  const int i = single ? 0 : u - ((q0 >> SHIFT) + 2 * b);  // touched block of the request
   const int ctx = len - ql;
   const int64_t first = (static_cast<int64_t>(ctx >> SHIFT) + i) << SHIFT;  // first position of the block
   if (i < 0 || first >= len) return;
   const int phys = ld_cg(p.block_tables + static_cast<int64_t>(b) * p.max_blocks_per_seq + (first >> SHIFT));
   if (phys < 0 || phys >= p.num_blocks) {
-    if (lane == 0) flag_error(p.status, PA_FLAG_BLOCK_RANGE);
+    if (report) flag_error(p.status, PA_FLAG_BLOCK_RANGE);
     return;
   }
-  const int row0 = max(ctx - static_cast<int>(first), 0);        // rows [row0, row1) of the block are new
-  const int row1 = min(len - static_cast<int>(first), BS);
+  const int row0 = max(ctx - static_cast<int>(first), 0);  // rows [row0, row1) of the block are new
+  const int row1 = static_cast<int>(min(static_cast<long long>(len) - first, static_cast<long long>(BS)));
   const int64_t token0 = q0 + (first + row0 - ctx);
-  const int64_t stride8 = (is_v ? p.value_stride : p.key_stride) / 8;
-  const uint4 *src = static_cast<const uint4 *>(is_v ? p.value : p.key) + token0 * stride8 +
-                     static_cast<int64_t>(kvh) * CPR;
-  float *scale_at = (is_v ? p.v_scales : p.k_scales) + static_cast<int64_t>(phys) * p.num_kv_heads + kvh;
-  float before = row0 > 0 ? ld_cg(scale_at) : 0.f;
-
   const int n = (row1 - row0) * CPR;
-  uint4 x[NV];
-#pragma unroll
-  for (int j = 0; j < NV; ++j) {
-    const int k = lane + 32 * j, row = k / CPR, c = k % CPR;
-    x[j] = make_uint4(0u, 0u, 0u, 0u);
-    if (k < n) x[j] = ld_cg(src + row * stride8 + c);
-  }
-  uint32_t m2 = 0;
-#pragma unroll
-  for (int j = 0; j < NV; ++j) {
-    m2 = __vmaxu2(m2, __vmaxu2(finite_magnitudes<E>(x[j].x), finite_magnitudes<E>(x[j].y)));
-    m2 = __vmaxu2(m2, __vmaxu2(finite_magnitudes<E>(x[j].z), finite_magnitudes<E>(x[j].w)));
-  }
-  const uint32_t m = __reduce_max_sync(0xffffffffu, max(m2 & 0xffffu, m2 >> 16));
-  // a scale that is no positive finite number (never written) counts as 0
-  if (!(before > 0.f && before <= 3.4028234e38f)) before = 0.f;
-  const float after = fmaxf(before, needed_scale(E::lo(m)));
-
   const int64_t row8 = static_cast<int64_t>(p.num_kv_heads) * CPR;  // 8-code vectors per cache row
-  uint2 *dst = static_cast<uint2 *>(is_v ? p.value_cache : p.key_cache) + static_cast<int64_t>(phys) * BS * row8 +
-               static_cast<int64_t>(kvh) * CPR;
+
+  for (int r = warp; r < 2 * p.num_kv_heads; r += warps) {
+    const bool is_v = r >= p.num_kv_heads;
+    const int kvh = is_v ? r - p.num_kv_heads : r;
+    const int64_t stride8 = (is_v ? p.value_stride : p.key_stride) / 8;
+    const uint4 *src = static_cast<const uint4 *>(is_v ? p.value : p.key) + token0 * stride8 +
+                       static_cast<int64_t>(kvh) * CPR;
+    float *scale_at = (is_v ? p.v_scales : p.k_scales) + static_cast<int64_t>(phys) * p.num_kv_heads + kvh;
+    float before = row0 > 0 ? ld_cg(scale_at) : 0.f;
+    uint4 x[NV];
 #pragma unroll
-  for (int j = 0; j < NV; ++j) {
-    const int k = lane + 32 * j, row = k / CPR, c = k % CPR;
-    if (k < n) dst[(row0 + row) * row8 + c] = quantize8<E>(x[j], after);
-  }
-  if (row0 > 0 && after != before) {  // the rows already there, under the larger scale
-    const float ratio = before / after;
-    for (int k = lane; k < row0 * CPR; k += 32) {
-      uint2 *at = dst + (k / CPR) * row8 + k % CPR;
-      const uint2 v = *at;
-      *at = make_uint2(rescale4(v.x, ratio), rescale4(v.y, ratio));
+    for (int j = 0; j < NV; ++j) {
+      const int k = lane + 32 * j, row = k / CPR, c = k % CPR;
+      x[j] = make_uint4(0u, 0u, 0u, 0u);
+      if (k < n) x[j] = ld_cg(src + row * stride8 + c);
     }
+    uint32_t m2 = 0;
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      m2 = __vmaxu2(m2, __vmaxu2(finite_magnitudes<E>(x[j].x), finite_magnitudes<E>(x[j].y)));
+      m2 = __vmaxu2(m2, __vmaxu2(finite_magnitudes<E>(x[j].z), finite_magnitudes<E>(x[j].w)));
+    }
+    const uint32_t m = __reduce_max_sync(0xffffffffu, max(m2 & 0xffffu, m2 >> 16));
+    // a scale that is no positive finite number (never written) counts as 0
+    if (!(before > 0.f && before <= 3.4028234e38f)) before = 0.f;
+    const float after = fmaxf(before, needed_scale(E::lo(m)));
+    const bool power_of_two = (__float_as_uint(after) & 0x7FFFFFu) == 0;
+    const float inverse = __frcp_rn(after);
+
+    uint2 *dst = static_cast<uint2 *>(is_v ? p.value_cache : p.key_cache) + static_cast<int64_t>(phys) * BS * row8 +
+                 static_cast<int64_t>(kvh) * CPR;
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      const int k = lane + 32 * j, row = k / CPR, c = k % CPR;
+      if (k < n) dst[(row0 + row) * row8 + c] = quantize8_by<E>(x[j], after, inverse, power_of_two);
+    }
+    if (row0 > 0 && after != before) {  // the rows already there, under the larger scale
+      const float ratio = before / after;
+      for (int k = lane; k < row0 * CPR; k += 32) {
+        uint2 *at = dst + (k / CPR) * row8 + k % CPR;
+        const uint2 v = *at;
+        *at = make_uint2(rescale4(v.x, ratio), rescale4(v.y, ratio));
+      }
+    }
+    if (lane == 0) *scale_at = after;
   }
-  if (lane == 0) *scale_at = after;
 }
 
 template <int D, int BS, typename E>
 cudaError_t launch_scatter(const BlockScatterLaunch &p, cudaStream_t stream) {
   const int64_t units =
       p.max_query_len <= 1 ? p.num_seqs : p.total_q / BS + 2 * static_cast<int64_t>(p.num_seqs);
-  const int64_t ctas = (units * 2 * p.num_kv_heads + kScatterWarps - 1) / kScatterWarps;
-  return launch_pdl(block_scatter_kernel<D, BS, E>, dim3(static_cast<unsigned>(ctas)), dim3(kScatterWarps * 32), 0,
-                    stream, p);
+  const int warps = 2 * p.num_kv_heads < kScatterWarps ? 2 * p.num_kv_heads : kScatterWarps;
+  return launch_pdl(block_scatter_kernel<D, BS, E>, dim3(static_cast<unsigned>(units)), dim3(warps * 32), 0, stream,
+                    p);
 }
 
 template <int D, typename E>

@@ -135,6 +135,8 @@ __global__ void __launch_bounds__(kNormRopeWarps * 32, kNormRopeCtas) norm_rope_
       for (int k = 0; k < kRowBatch; ++k) {
         const int row = (g0 + k) * RPW + row_in_group;
         const bool is_q = row < p.num_heads, is_v = row >= p.num_heads + p.num_kv_heads;
+        uint4 oa = xa[k], ob = xb[k];
+        if (DST == kRows || !__all_sync(FULL, is_v)) {  // V rows are copied as they are
         float a[8], b[8];
         widen8<E>(xa[k], a);
         widen8<E>(xb[k], b);
@@ -185,8 +187,12 @@ __global__ void __launch_bounds__(kNormRopeWarps * 32, kNormRopeCtas) norm_rope_
             }
           }
         }
+        if (!is_v) {
+          oa = narrow8<E>(a);
+          ob = narrow8<E>(b);
+        }
+        }
         if (g0 + k >= g_end || row >= rows) continue;
-        const uint4 oa = is_v ? xa[k] : narrow8<E>(a), ob = is_v ? xb[k] : narrow8<E>(b);
         if (is_q) {
           uint4 *dst = static_cast<uint4 *>(p.q_out) + t * (p.q_out_stride / 8) + static_cast<int64_t>(row) * d8;
           if (has_a) dst[ca] = oa;
