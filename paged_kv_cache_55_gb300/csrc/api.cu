@@ -184,7 +184,8 @@ size_t pa_attention_workspace_size(int32_t num_seqs, int32_t total_q_tokens, int
   pa::BlockWorkspace wb;
   if (!pa::workspace_layout(num_seqs, total_q_tokens, max_seq_len, num_heads, num_kv_heads, head_dim, false, w16) ||
       !pa::workspace_layout(num_seqs, total_q_tokens, max_seq_len, num_heads, num_kv_heads, head_dim, true, w8) ||
-      !pa::block_workspace_layout(num_seqs, total_q_tokens, max_seq_len, num_heads, num_kv_heads, head_dim, wb))
+      !pa::block_workspace_layout(num_seqs, total_q_tokens, max_query_len, max_seq_len, num_heads, num_kv_heads,
+                                  head_dim, wb))
     return 0;
   const size_t w = w16.total > w8.total ? w16.total : w8.total;
   return w > wb.total ? w : wb.total;
@@ -238,7 +239,8 @@ pa_status attention_call(const void *q, int64_t q_token_stride, const void *key_
   size_t need = 0;
   if (k_scales) {
     pa::BlockWorkspace w;
-    if (!pa::block_workspace_layout(num_seqs, total_q_tokens, max_seq_len, num_heads, num_kv_heads, head_dim, w))
+    if (!pa::block_workspace_layout(num_seqs, total_q_tokens, max_query_len, max_seq_len, num_heads, num_kv_heads,
+                                    head_dim, w))
       return PA_ERR_DIMS;
     need = w.total;
   } else {

@@ -90,13 +90,29 @@ __host__ __device__ inline int64_t unit_tiles(int64_t total, int64_t pairs, int6
   return u < 1 ? 1 : u;
 }
 
+// Prefill tiles over fewer than 3/4 of the SMs are split over their keys, so
+// that no SM idles while others walk a long context: into parts of `ranges`
+// 128-key ranges (at least kMinRanges: a unit's start and its partial cost
+// about one), few enough for one unit per SM. With t tiles and R ranges in all,
+// sum ceil(ranges of a tile / u) <= R / u + t <= SMs / KV heads for u = R /
+// (SMs / KV heads - t). Merged like the decode partials.
+constexpr int kSplitSms = 152, kMinRanges = 2, kRangeKeys = 128;
+constexpr int kNoSplit = 1 << 30;
+__host__ __device__ inline int part_items(int num_kv_heads) { return kSplitSms / num_kv_heads; }
+__device__ __forceinline__ int part_ranges(int64_t tiles, int64_t ranges, int num_kv_heads) {
+  const int64_t slots = part_items(num_kv_heads);
+  if (tiles * 4 > slots * 3) return kNoSplit;
+  const int64_t u = (ranges + slots - tiles - 1) / (slots - tiles);
+  return static_cast<int>(u < kMinRanges ? kMinRanges : u);
+}
+
 struct PlanParams {
   const int32_t *seq_lens, *query_start_loc;
   int32_t num_seqs, total_q, max_query_len, max_seq_len, max_blocks_per_seq, block_size;
   int32_t num_kv_heads;
   int32_t rows_per_item;  // 8 / G
   int32_t tile_pos;       // query positions per prefill tile
-  int32_t max_items, max_tiles;
+  int32_t max_items, max_tiles, max_part_items;
   int64_t warps;          // unit_warps
   int32_t first_units;    // units the decode warps take without the queue
   int32_t *nparts, *first_full, *rest;  // per request: partitions, item of the first full one, of the partial last (or -1)
@@ -126,8 +142,12 @@ struct DecodeParams {
 
 struct MergeParams {
   const int32_t *query_start_loc, *nparts, *first_full, *rest;
-  int32_t num_kv_heads, num_heads, max_items;
+  int32_t num_kv_heads, num_heads, num_seqs, max_items, total_q;
   const float *part_o, *part_lse;
+  const int4 *tiles;  // prefill tiles (none launched: tile_items 0)
+  const int32_t *tile_count;
+  int32_t tile_items;  // that may be parts
+  const float *tile_o, *tile_lse;
   bf16 *out;
 };
 
@@ -242,6 +262,30 @@ __global__ void __launch_bounds__(NT) block_plan_kernel(const PlanParams p) {
   unsigned long long full_total;
   block_scan<NT>(mine, warp_tot, &full_total);
   const int all_full = static_cast<int>(min(full_total, static_cast<unsigned long long>(p.max_items)));
+  // parts of the prefill tiles
+  const bool chunks = p.max_query_len > p.rows_per_item;
+  int split = kNoSplit;  // ranges per part
+  auto tile_ranges = [&](int len, int ql, int t) {  // 128-key ranges that tile t of a request walks
+    return (len - ql + min((t + 1) * p.tile_pos, ql) - 1) / kRangeKeys + 1;
+  };
+  if (chunks && p.max_part_items > 0) {
+    unsigned long long tiles, ranges;
+    mine = 0;
+    for (int b = tid; b < p.num_seqs; b += NT) {
+      if (!once) r = read_request(p, b, false);
+      mine += r.tiles;
+    }
+    block_scan<NT>(mine, warp_tot, &tiles);
+    if (tiles > 0 && tiles * 4 <= static_cast<unsigned long long>(part_items(p.num_kv_heads)) * 3) {
+      mine = 0;
+      for (int b = tid; b < p.num_seqs; b += NT) {
+        if (!once) r = read_request(p, b, false);
+        for (int t = 0; t < r.tiles; ++t) mine += tile_ranges(r.len, r.ql, t);
+      }
+      block_scan<NT>(mine, warp_tot, &ranges);
+      split = part_ranges(static_cast<int64_t>(tiles), static_cast<int64_t>(ranges), p.num_kv_heads);
+    }
+  }
   int carry_full = 0, carry_rest = 0, carry_tile = 0;
   for (int base = 0; base < p.num_seqs; base += NT) {
     const int b = base + tid, n = min(NT, p.num_seqs - base);
@@ -255,7 +299,16 @@ __global__ void __launch_bounds__(NT) block_plan_kernel(const PlanParams p) {
     const unsigned long long ex =
         block_scan<NT>(static_cast<unsigned long long>(full) | (static_cast<unsigned long long>(rest) << 40), warp_tot,
                        &tot);
-    const unsigned long long ex_tile = block_scan<NT>(static_cast<unsigned long long>(r.tiles), warp_tot, &tile_tot);
+    unsigned long long ex_tile = 0;
+    tile_tot = 0;
+    if (chunks) {
+      unsigned long long n_parts = r.tiles;
+      if (split != kNoSplit) {
+        n_parts = 0;
+        for (int t = 0; t < r.tiles; ++t) n_parts += (tile_ranges(r.len, r.ql, t) + split - 1) / split;
+      }
+      ex_tile = block_scan<NT>(n_parts, warp_tot, &tile_tot);
+    }
     const int ex_full = static_cast<int>(ex & ((1ull << 40) - 1)), n_full = static_cast<int>(tot & ((1ull << 40) - 1));
     const int n_tile = static_cast<int>(tile_tot);
     pre_full[tid] = ex_full;
@@ -289,11 +342,25 @@ __global__ void __launch_bounds__(NT) block_plan_kernel(const PlanParams p) {
       if (tile >= p.max_tiles) break;
       // a request's last tiles see the most keys: queue them first
       const int k = find_range(pre_tile, n, i);
-      const int ql = s_ql[k], nt = (ql + p.tile_pos - 1) / p.tile_pos;
-      const int r0 = (nt - 1 - (i - pre_tile[k])) * p.tile_pos;
-      const int npos = min(p.tile_pos, ql - r0), pos0 = (s_len[k] - ql) + r0;
+      const int ql = s_ql[k], len = s_len[k], nt = (ql + p.tile_pos - 1) / p.tile_pos;
+      int t = nt - 1, part = i - pre_tile[k], parts = 1;
+      if (split == kNoSplit) {
+        t -= part;
+        part = 0;
+      } else {
+        for (;; --t) {
+          parts = (tile_ranges(len, ql, t) + split - 1) / split;
+          if (part < parts || t == 0) break;
+          part -= parts;
+        }
+      }
+      const int r0 = t * p.tile_pos, npos = min(p.tile_pos, ql - r0), pos0 = (len - ql) + r0, end = pos0 + npos;
       p.tiles[2 * tile] = make_int4(base + k, s_q0[k] + r0, npos, pos0);
-      p.tiles[2 * tile + 1] = make_int4(0, pos0 + npos, -1, 1);
+      p.tiles[2 * tile + 1] =
+          parts > 1 ? make_int4(part * split * kRangeKeys,
+                                static_cast<int>(min(static_cast<long long>(end), (part + 1LL) * split * kRangeKeys)),
+                                part, parts)
+                    : make_int4(0, end, -1, 1);
     }
     carry_full += n_full;
     carry_rest += static_cast<int>(tot >> 40);
@@ -713,8 +780,9 @@ __global__ void __launch_bounds__(NWARPS * 32, 1)
         l[0] += __shfl_xor_sync(FULL, l[0], off);
         l[1] += __shfl_xor_sync(FULL, l[1], off);
       }
-      const float inv0 = l[0] > 0.f ? 1.f / l[0] : 0.f;
-      const float inv1 = l[1] > 0.f ? 1.f / l[1] : 0.f;
+      // (a NaN sum is no empty one: it reaches the output)
+      const float inv0 = l[0] != 0.f ? 1.f / l[0] : 0.f;
+      const float inv1 = l[1] != 0.f ? 1.f / l[1] : 0.f;
       if (cur.part < 0) {
         const int col = lane >> 2, qi = col / G, g = col % G;
         bf16 *dst = p.out + static_cast<int64_t>(cur.row0 + (qi < cur.nrows ? qi : 0)) * p.num_heads * D +
@@ -742,7 +810,7 @@ __global__ void __launch_bounds__(NWARPS * 32, 1)
               dst[16 * mt] = o[mt][c] * inv;
               dst[16 * mt + 8] = o[mt][2 + c] * inv;
             }
-            if (lane < 4) p.part_lse[base + col] = l[c] > 0.f ? m[c] + __log2f(l[c]) : -INFINITY;
+            if (lane < 4) p.part_lse[base + col] = l[c] != 0.f ? m[c] + __log2f(l[c]) : -INFINITY;
           }
         }
       }
@@ -769,96 +837,66 @@ __global__ void __launch_bounds__(NWARPS * 32, 1)
 // columns. A warp reads eight partitions at a time with a running maximum of
 // their log-sum-exps. Sixteen warps when the pairs are few (their partitions
 // are then many), four when there are several CTAs per SM anyway.
-template <int D, int G, typename E, int NW>
-__global__ void __launch_bounds__(NW * 32) block_merge_kernel(const MergeParams p) {
-  constexpr int EPL = (D + 31) / 32;  // outputs per lane (head_dim 80, 96: the last lanes' unused)
-  constexpr bool VEC4 = D % 128 == 0, VEC2 = D == 64;
-  __shared__ float s_m[NW], s_w[NW], s_acc[NW][32 * EPL];
-  griddep_wait();
-  griddep_launch_dependents();
-  const int b = blockIdx.x / p.num_kv_heads, kvh = blockIdx.x - b * p.num_kv_heads;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int np = ld_cg(p.nparts + b), full0 = ld_cg(p.first_full + b), rest = ld_cg(p.rest + b);
-  const int q0 = ld_cg(p.query_start_loc + b), ql = ld_cg(p.query_start_loc + b + 1) - q0;
-  if (np <= 1 || ql < 1 || ql * G > kCols) return;
-  const int cols = ql * G;
-  const int nc = cols <= 1 ? 1 : (cols <= 2 ? 2 : (cols <= 4 ? 4 : 8));
-  const int wc = nc < NW ? nc : NW;  // columns in parallel
-  const int sub = warp / wc, subs = NW / wc;
-  const int k_begin = np * sub / subs, k_end = np * (sub + 1) / subs;
-  for (int col0 = 0; col0 < cols; col0 += wc) {
-    const int col = col0 + warp % wc;
-    float M = -INFINITY, wsum = 0.f, acc[EPL];
+// A warp's lanes hold EPL outputs each (head_dim 80, 96: the last lanes' unused).
+template <int D>
+struct Merged {
+  static constexpr int EPL = (D + 31) / 32;
+  static constexpr bool VEC4 = D % 128 == 0, VEC2 = D == 64;
+  float M = -INFINITY, wsum = 0.f, acc[EPL];
+  __device__ __forceinline__ Merged() {
 #pragma unroll
     for (int e = 0; e < EPL; ++e) acc[e] = 0.f;
-    if (col < cols) {
-      for (int k0 = k_begin; k0 < k_end; k0 += 8) {
-        float lv[8], ov[8][EPL];
+  }
+  // partitions [begin, end): row at(k) of o and lse; a partition without keys
+  // (lse -inf) is left out, whatever its outputs hold
+  template <typename At>
+  __device__ __forceinline__ void add(int begin, int end, int lane, const float *lse, const float *o, At at) {
+    for (int k0 = begin; k0 < end; k0 += 8) {
+      float lv[8], ov[8][EPL];
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          const int k = min(k0 + j, k_end - 1);
-          const int item = min(max(k == np - 1 && rest >= 0 ? rest : full0 + k, 0), p.max_items - 1);
-          const int64_t at = (static_cast<int64_t>(item) * p.num_kv_heads + kvh) * kCols + col;
-          lv[j] = ld_cg(p.part_lse + at);
-          const float *src = p.part_o + at * D + lane * EPL;
-          if constexpr (VEC2) {
-            const float2 v = ld_cg(reinterpret_cast<const float2 *>(src));
-            ov[j][0] = v.x, ov[j][1] = v.y;
-          } else if constexpr (VEC4) {
+      for (int j = 0; j < 8; ++j) {
+        const int64_t row = at(min(k0 + j, end - 1));
+        lv[j] = ld_cg(lse + row);
+        const float *src = o + row * D + lane * EPL;
+        if constexpr (VEC2) {
+          const float2 v = ld_cg(reinterpret_cast<const float2 *>(src));
+          ov[j][0] = v.x, ov[j][1] = v.y;
+        } else if constexpr (VEC4) {
 #pragma unroll
-            for (int e = 0; e < EPL; e += 4) {
-              const float4 v = ld_cg(reinterpret_cast<const float4 *>(src + e));
-              ov[j][e] = v.x, ov[j][e + 1] = v.y, ov[j][e + 2] = v.z, ov[j][e + 3] = v.w;
-            }
-          } else {
-#pragma unroll
-            for (int e = 0; e < EPL; ++e) ov[j][e] = lane * EPL + e < D ? ld_cg(src + e) : 0.f;
+          for (int e = 0; e < EPL; e += 4) {
+            const float4 v = ld_cg(reinterpret_cast<const float4 *>(src + e));
+            ov[j][e] = v.x, ov[j][e + 1] = v.y, ov[j][e + 2] = v.z, ov[j][e + 3] = v.w;
           }
+        } else {
+#pragma unroll
+          for (int e = 0; e < EPL; ++e) ov[j][e] = lane * EPL + e < D ? ld_cg(src + e) : 0.f;
         }
-        float Mn = M;
+      }
+      float Mn = M;
 #pragma unroll
-        for (int j = 0; j < 8; ++j)
-          if (k0 + j < k_end) Mn = fmaxf(Mn, lv[j]);
-        const float Ms = Mn == -INFINITY ? 0.f : Mn;
-        const float r = ex2_approx(M - Ms);
-        wsum *= r;
+      for (int j = 0; j < 8; ++j)
+        if (k0 + j < end) Mn = fmaxf(Mn, lv[j]);
+      const float Ms = Mn == -INFINITY ? 0.f : Mn;
+      const float r = ex2_approx(M - Ms);
+      wsum *= r;
 #pragma unroll
-        for (int e = 0; e < EPL; ++e) acc[e] *= r;
-        M = Mn;
+      for (int e = 0; e < EPL; ++e) acc[e] *= r;
+      M = Mn;
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          if (k0 + j < k_end) {
-            const float w = ex2_approx(lv[j] - Ms);
-            wsum += w;
+      for (int j = 0; j < 8; ++j) {
+        if (k0 + j < end && lv[j] != -INFINITY) {
+          const float w = ex2_approx(lv[j] - Ms);
+          wsum += w;
 #pragma unroll
-            for (int e = 0; e < EPL; ++e) acc[e] += w * ov[j][e];
-          }
+          for (int e = 0; e < EPL; ++e) acc[e] += w * ov[j][e];
         }
       }
     }
-    if (subs > 1) {  // then one round of columns
-      if (lane == 0) {
-        s_m[warp] = M;
-        s_w[warp] = wsum;
-      }
-#pragma unroll
-      for (int e = 0; e < EPL; ++e) s_acc[warp][e * 32 + lane] = acc[e];
-      __syncthreads();
-      if (sub > 0) return;
-      for (int k = 1; k < subs; ++k) {
-        const int w = k * wc + warp;
-        const float Mo = s_m[w], Mn = fmaxf(M, Mo), Ms = Mn == -INFINITY ? 0.f : Mn;
-        const float ra = ex2_approx(M - Ms), rb = ex2_approx(Mo - Ms);
-        wsum = wsum * ra + s_w[w] * rb;
-#pragma unroll
-        for (int e = 0; e < EPL; ++e) acc[e] = acc[e] * ra + s_acc[w][e * 32 + lane] * rb;
-        M = Mn;
-      }
-    }
-    if (col >= cols) continue;
-    const float inv = wsum > 0.f ? 1.f / wsum : 0.f;
-    bf16 *dst = p.out + static_cast<int64_t>(q0 + col / G) * p.num_heads * D +
-                static_cast<int64_t>(kvh * G + col % G) * D + lane * EPL;
+  }
+  template <typename E>
+  __device__ __forceinline__ void store(bf16 *row, int lane) const {
+    const float inv = wsum > 0.f ? 1.f / wsum : (wsum == 0.f ? 0.f : wsum);  // NaN stays NaN
+    bf16 *dst = row + lane * EPL;
     if constexpr (VEC2) {
       *reinterpret_cast<uint32_t *>(dst) = E::pack(acc[0] * inv, acc[1] * inv);
     } else if constexpr (VEC4) {
@@ -873,6 +911,79 @@ __global__ void __launch_bounds__(NW * 32) block_merge_kernel(const MergeParams 
           *reinterpret_cast<unsigned short *>(dst + e) =
               static_cast<unsigned short>(E::pack(acc[e] * inv, 0.f) & 0xffffu);
     }
+  }
+};
+
+constexpr int kTileMergeCtas = 8;  // CTAs that share the rows of one split prefill tile
+
+template <int D, int G, typename E, int NW>
+__global__ void __launch_bounds__(NW * 32) block_merge_kernel(const MergeParams p) {
+  constexpr int EPL = Merged<D>::EPL;
+  __shared__ float s_m[NW], s_w[NW], s_acc[NW][32 * EPL];
+  griddep_wait();
+  griddep_launch_dependents();
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int pairs = p.num_seqs * p.num_kv_heads;
+  if (static_cast<int>(blockIdx.x) >= pairs) {
+    // a split prefill tile: a warp per row
+    const int i = blockIdx.x - pairs, item = i / (p.num_kv_heads * kTileMergeCtas);
+    const int kvh = (i / kTileMergeCtas) % p.num_kv_heads, rb = i % kTileMergeCtas;
+    if (item >= min(ld_cg(p.tile_count), p.tile_items)) return;
+    const int4 r0 = ld_cg(p.tiles + 2 * item), r1 = ld_cg(p.tiles + 2 * item + 1);
+    const int row0 = r0.y, npos = r0.z, parts = r1.w;
+    constexpr int ROWS = prefill_tile_rows(D);
+    if (r1.z != 0 || parts <= 1 || item + parts > p.tile_items) return;  // the tile's first part speaks for it
+    if (row0 < 0 || npos < 1 || npos * G > ROWS || row0 + npos > p.total_q) return;
+    for (int row = rb * NW + warp; row < npos * G; row += kTileMergeCtas * NW) {
+      Merged<D> m;
+      m.add(0, parts, lane, p.tile_lse, p.tile_o, [&](int k) {
+        return (static_cast<int64_t>(item + k) * p.num_kv_heads + kvh) * ROWS + row;
+      });
+      m.template store<E>(p.out + static_cast<int64_t>(row0 + row / G) * p.num_heads * D +
+                              static_cast<int64_t>(kvh * G + row % G) * D,
+                          lane);
+    }
+    return;
+  }
+  const int b = blockIdx.x / p.num_kv_heads, kvh = blockIdx.x - b * p.num_kv_heads;
+  const int np = ld_cg(p.nparts + b), full0 = ld_cg(p.first_full + b), rest = ld_cg(p.rest + b);
+  const int q0 = ld_cg(p.query_start_loc + b), ql = ld_cg(p.query_start_loc + b + 1) - q0;
+  if (np <= 1 || ql < 1 || ql * G > kCols) return;
+  const int cols = ql * G;
+  const int nc = cols <= 1 ? 1 : (cols <= 2 ? 2 : (cols <= 4 ? 4 : 8));
+  const int wc = nc < NW ? nc : NW;  // columns in parallel
+  const int sub = warp / wc, subs = NW / wc;
+  for (int col0 = 0; col0 < cols; col0 += wc) {
+    const int col = col0 + warp % wc;
+    Merged<D> m;
+    if (col < cols)
+      m.add(np * sub / subs, np * (sub + 1) / subs, lane, p.part_lse, p.part_o, [&](int k) {
+        const int item = min(max(k == np - 1 && rest >= 0 ? rest : full0 + k, 0), p.max_items - 1);
+        return (static_cast<int64_t>(item) * p.num_kv_heads + kvh) * kCols + col;
+      });
+    if (subs > 1) {  // then there is one round of columns
+      if (lane == 0) {
+        s_m[warp] = m.M;
+        s_w[warp] = m.wsum;
+      }
+#pragma unroll
+      for (int e = 0; e < EPL; ++e) s_acc[warp][e * 32 + lane] = m.acc[e];
+      __syncthreads();
+      if (sub > 0) return;
+      for (int k = 1; k < subs; ++k) {
+        const int w = k * wc + warp;
+        const float Mo = s_m[w], Mn = fmaxf(m.M, Mo), Ms = Mn == -INFINITY ? 0.f : Mn;
+        const float ra = ex2_approx(m.M - Ms), rb = ex2_approx(Mo - Ms);
+        m.wsum = m.wsum * ra + s_w[w] * rb;
+#pragma unroll
+        for (int e = 0; e < EPL; ++e) m.acc[e] = m.acc[e] * ra + s_acc[w][e * 32 + lane] * rb;
+        m.M = Mn;
+      }
+    }
+    if (col < cols)
+      m.template store<E>(p.out + static_cast<int64_t>(q0 + col / G) * p.num_heads * D +
+                              static_cast<int64_t>(kvh * G + col % G) * D,
+                          lane);
   }
 }
 
@@ -938,6 +1049,7 @@ cudaError_t launch_typed(const AttnLaunch &a, const BlockWorkspace &w, cudaStrea
   pp.tile_pos = prefill_tile_rows(D) / G;
   pp.max_items = w.max_items;
   pp.max_tiles = w.max_tiles;
+  pp.max_part_items = w.part_items;
   pp.warps = unit_warps(D);
   pp.first_units = static_cast<int32_t>(grid * NW);
   pp.nparts = reinterpret_cast<int32_t *>(ws + w.nparts);
@@ -1010,6 +1122,9 @@ cudaError_t launch_typed(const AttnLaunch &a, const BlockWorkspace &w, cudaStrea
     tp.max_tiles = w.max_tiles;
     tp.k_scales = a.k_scales;
     tp.v_scales = a.v_scales;
+    tp.max_part_items = w.part_items;
+    tp.part_o = reinterpret_cast<float *>(ws + w.tile_o);
+    tp.part_lse = reinterpret_cast<float *>(ws + w.tile_lse);
     tp.status = a.status;
     if (a.tile_start) cudaEventRecord(a.tile_start, stream);
     err = launch_prefill_tiles<D, G, E, true, true>(kmap, vmap, vmap, tp, a.sm_count, stream);
@@ -1026,15 +1141,23 @@ cudaError_t launch_typed(const AttnLaunch &a, const BlockWorkspace &w, cudaStrea
     mp.rest = pp.rest;
     mp.num_kv_heads = a.num_kv_heads;
     mp.num_heads = a.num_heads;
+    mp.num_seqs = a.num_seqs;
     mp.max_items = w.max_items;
+    mp.total_q = a.total_q;
+    mp.tiles = pp.tiles;
+    mp.tile_count = pp.counts + 2;
+    mp.tile_items = tiles_follow ? w.part_items : 0;
+    mp.tile_o = reinterpret_cast<float *>(ws + w.tile_o);
+    mp.tile_lse = reinterpret_cast<float *>(ws + w.tile_lse);
     mp.part_o = dp.part_o;
     mp.part_lse = dp.part_lse;
     mp.out = dp.out;
     const unsigned pairs = static_cast<unsigned>(a.num_seqs * a.num_kv_heads);
+    const unsigned ctas = pairs + static_cast<unsigned>(mp.tile_items * a.num_kv_heads * kTileMergeCtas);
     if (pairs <= 2u * static_cast<unsigned>(a.sm_count))
-      err = launch_pdl(block_merge_kernel<D, G, E, 16>, dim3(pairs), dim3(16 * 32), 0, stream, mp);
+      err = launch_pdl(block_merge_kernel<D, G, E, 16>, dim3(ctas), dim3(16 * 32), 0, stream, mp);
     else
-      err = launch_pdl(block_merge_kernel<D, G, E, 4>, dim3(pairs), dim3(4 * 32), 0, stream, mp);
+      err = launch_pdl(block_merge_kernel<D, G, E, 4>, dim3(ctas), dim3(4 * 32), 0, stream, mp);
     if (err != cudaSuccess) return err;
     ++*launched;
   }
@@ -1043,8 +1166,8 @@ cudaError_t launch_typed(const AttnLaunch &a, const BlockWorkspace &w, cudaStrea
 
 }  // namespace
 
-bool block_workspace_layout(int32_t num_seqs, int32_t total_q, int32_t max_seq_len, int32_t num_heads,
-                            int32_t num_kv_heads, int32_t head_dim, BlockWorkspace &w) {
+bool block_workspace_layout(int32_t num_seqs, int32_t total_q, int32_t max_query_len, int32_t max_seq_len,
+                            int32_t num_heads, int32_t num_kv_heads, int32_t head_dim, BlockWorkspace &w) {
   if (num_seqs < 0 || total_q < 0 || max_seq_len < 0 || num_heads <= 0 || num_kv_heads <= 0 || head_dim <= 0 ||
       num_heads % num_kv_heads != 0 || num_heads / num_kv_heads > kCols)
     return false;
@@ -1061,7 +1184,17 @@ bool block_workspace_layout(int32_t num_seqs, int32_t total_q, int32_t max_seq_l
       static_cast<int64_t>(num_seqs) * num_kv_heads > (1LL << 30))
     return false;
   w.max_items = static_cast<int32_t>(items > 0 ? items : 1);
-  w.max_tiles = static_cast<int32_t>(tiles > 0 ? tiles : 1);
+  // parts of split prefill tiles: at least kMinRanges ranges each
+  int64_t split_items = 0;
+  if (max_query_len > kCols / G) {
+    const int64_t most = (static_cast<int64_t>(max_seq_len) + kMinRanges * kRangeKeys - 1) / (kMinRanges * kRangeKeys);
+    split_items = part_items(num_kv_heads);
+    if (most <= 1) split_items = 0;
+    if (most * tiles < split_items) split_items = most * tiles;
+  }
+  w.part_items = static_cast<int32_t>(split_items);
+  const int64_t tile_items = tiles > split_items ? tiles : split_items;
+  w.max_tiles = static_cast<int32_t>(tile_items > 0 ? tile_items : 1);
   const size_t per_seq = align256(sizeof(int32_t) * (static_cast<size_t>(num_seqs) + 1));
   const size_t parts = static_cast<size_t>(w.max_items) * num_kv_heads * kCols;
   size_t off = 0;
@@ -1073,13 +1206,17 @@ bool block_workspace_layout(int32_t num_seqs, int32_t total_q, int32_t max_seq_l
   w.tiles = off;      off += align256(sizeof(int4) * 2 * static_cast<size_t>(w.max_tiles));
   w.part_lse = off;   off += align256(sizeof(float) * parts);
   w.part_o = off;     off += align256(sizeof(float) * parts * head_dim);
+  const size_t tile_rows = static_cast<size_t>(split_items) * num_kv_heads * rows;
+  w.tile_lse = off;   off += align256(sizeof(float) * tile_rows);
+  w.tile_o = off;     off += align256(sizeof(float) * tile_rows * head_dim);
   w.total = off;
   return true;
 }
 
 cudaError_t launch_block_attention(const AttnLaunch &a, cudaStream_t stream, int *launched) {
   BlockWorkspace w;
-  if (!block_workspace_layout(a.num_seqs, a.total_q, a.max_seq_len, a.num_heads, a.num_kv_heads, a.head_dim, w))
+  if (!block_workspace_layout(a.num_seqs, a.total_q, a.max_query_len, a.max_seq_len, a.num_heads, a.num_kv_heads,
+                              a.head_dim, w))
     return cudaErrorInvalidValue;
   const int G = a.num_heads / a.num_kv_heads;
 #define PA_DISPATCH(DD, GG)                                                               \

@@ -42,6 +42,14 @@ struct TileParams {
   int32_t max_tiles;
   const float *k_scales = nullptr;  // 8-bit caches with block scales: [num_blocks][Hkv]
   const float *v_scales = nullptr;
+  // block scales: tiles may be split over their keys. Records {b, first query
+  // token, positions, absolute position of the first}, {key begin, key end,
+  // part (-1: the whole tile), parts}; the rows of a part of item i < max_part_items
+  // and KV head h go to slot i * Hkv + h of tile-rows rows (normalised outputs,
+  // fp32, and their log2-sum-exp).
+  int32_t max_part_items = 0;
+  float *part_o = nullptr;    // [slots][tile rows][D]
+  float *part_lse = nullptr;  // [slots][tile rows]
   unsigned int *status;
 };
 

@@ -458,9 +458,18 @@ __device__ __forceinline__ void st_scales(uint32_t addr, float ks, float lv) {
 }
 
 // A published unit: a tile of one request and one KV head, or the end of the stream.
+// With block scales a unit may be a part of a tile's keys (kv_begin a multiple
+// of 128) whose rows go to partial slot `slot` (-1: the output).
 struct TileUnit {
-  int b, row0, npos, pos0, kv_end, kvh, stop;
+  int b, row0, npos, pos0, kv_end, kvh, stop, kv_begin, slot;
 };
+
+// The key range of a unit with block scales: a whole tile's keys, or a part of
+// them with a partial slot that exists.
+__device__ __forceinline__ bool part_sane(const TileUnit &r, const TileParams &p, int item) {
+  if (r.kv_begin < 0 || r.kv_begin % kKeyTile != 0 || r.kv_begin >= r.kv_end || r.kv_end > r.pos0 + r.npos) return false;
+  return r.slot < 0 ? r.kv_begin == 0 && r.kv_end == r.pos0 + r.npos : item < p.max_part_items;
+}
 
 // A bf16 V range in shared memory, rewritten by the two converter warps:
 // converter warp w takes its 16-byte chunks c = w * PER * 32 + lane + 32 i
@@ -654,13 +663,14 @@ __global__ void __launch_bounds__(KV8 ? kTileThreads8 : kTileThreads, 1)
     r.stop = 1;
     if (!failed) {
       const volatile int *u = units + 8 * s;
-      r.b = u[0];
+      r.slot = u[0];
       r.row0 = u[1];
       r.npos = u[2];
       r.pos0 = u[3];
       r.kv_end = u[4];
       r.kvh = u[5];
       r.stop = u[6];
+      r.kv_begin = BSC ? u[7] : 0;
     }
     __syncwarp();
     if (lane == 0 && !failed) mbar_arrive(bar(Lay::B_UE + s));
@@ -670,9 +680,14 @@ __global__ void __launch_bounds__(KV8 ? kTileThreads8 : kTileThreads, 1)
 #pragma unroll
     for (int h = 0; h < kHalves; ++h) {
       const int last = min(r.npos, (h + 1) * POS_PER_HALF);  // positions [h * POS_PER_HALF, last)
-      nh[h] = last > h * POS_PER_HALF ? (r.pos0 + last + kKeyTile - 1) / kKeyTile : 0;
+      if constexpr (BSC)  // of this part
+        nh[h] = last > h * POS_PER_HALF
+                    ? max((min(r.pos0 + last, r.kv_end) - r.kv_begin + kKeyTile - 1) / kKeyTile, 0)
+                    : 0;
+      else
+        nh[h] = last > h * POS_PER_HALF ? (r.pos0 + last + kKeyTile - 1) / kKeyTile : 0;
     }
-    return (r.kv_end + kKeyTile - 1) / kKeyTile;
+    return (r.kv_end - (BSC ? r.kv_begin : 0) + kKeyTile - 1) / kKeyTile;
   };
   // V in shared memory. VBLK: block after block of R = block_size rows, each
   // [atom][R rows][128 B]; else [atom][128 keys][128 B] (per-atom boxes).
@@ -698,7 +713,7 @@ __global__ void __launch_bounds__(KV8 ? kTileThreads8 : kTileThreads, 1)
       int u = 0;
       if (lane == 0) u = atomicAdd(p.tile_counter, 1);
       u = __shfl_sync(FULL, u, 0);
-      TileUnit r{0, 0, 0, 0, 0, 0, u >= total_units ? 1 : 0};
+      TileUnit r{0, 0, 0, 0, 0, 0, u >= total_units ? 1 : 0, 0, -1};
       if (!r.stop) {
         const int item = u / Hkv;
         r.kvh = u - item * Hkv;
@@ -709,9 +724,13 @@ __global__ void __launch_bounds__(KV8 ? kTileThreads8 : kTileThreads, 1)
         r.npos = r0.z;
         r.pos0 = r0.w;
         r.kv_end = r1.y;
+        if constexpr (BSC) {
+          r.kv_begin = r1.x;
+          r.slot = r1.z >= 0 ? item * Hkv + r.kvh : -1;
+        }
         const bool sane = r.b >= 0 && r.b < p.num_seqs && r.npos >= 1 && r.npos <= kPrefillTileRows / G &&
                           r.row0 >= 0 && r.row0 + r.npos <= p.total_q && r.pos0 >= 0 &&
-                          r.kv_end == r.pos0 + r.npos &&
+                          (BSC ? part_sane(r, p, item) : r.kv_end == r.pos0 + r.npos) &&
                           r.kv_end <= static_cast<int64_t>(p.max_blocks_per_seq) * bs;
         if (!sane) {
           if (lane == 0) flag_error(p.status, PA_FLAG_LENGTHS);
@@ -723,13 +742,14 @@ __global__ void __launch_bounds__(KV8 ? kTileThreads8 : kTileThreads, 1)
       if (failed) break;
       if (lane == 0) {
         volatile int *d = units + 8 * s;
-        d[0] = r.b;
+        d[0] = BSC ? r.slot : -1;
         d[1] = r.row0;
         d[2] = r.npos;
         d[3] = r.pos0;
         d[4] = r.kv_end;
         d[5] = r.kvh;
         d[6] = r.stop;
+        if (BSC) d[7] = r.kv_begin;
         mbar_arrive(bar(Lay::B_UF + s));  // release: the record is visible to whoever sees the phase
       }
       __syncwarp();
@@ -753,11 +773,12 @@ __global__ void __launch_bounds__(KV8 ? kTileThreads8 : kTileThreads, 1)
       for (int kt = 0; kt < nkt && !failed; ++kt) {
         // lane i computes the row coordinate of K box i and V box i of this
         // range, and issues those boxes itself once lane 0 has set the byte count
-        const int zk = lane < nbk ? box_z(kt * kKeyTile + lane * box_rows, box_rows) : 0;
-        const int zv = VBLK ? (lane < nbv ? box_z(kt * kKeyTile + lane * bs, bs) : 0) : zk;
+        const int key0 = (BSC ? r.kv_begin : 0) + kt * kKeyTile;  // first key of the range
+        const int zk = lane < nbk ? box_z(key0 + lane * box_rows, box_rows) : 0;
+        const int zv = VBLK ? (lane < nbv ? box_z(key0 + lane * bs, bs) : 0) : zk;
         float gks = 1.f, gvs1 = 1.f;  // block scales of 8-key group `lane` (1 past the last key)
         if constexpr (BSC) {
-          if (lane < kKeyTile / 8) block_scales_of(p, table, kt * kKeyTile + 8 * lane, r.kv_end, r.kvh, gks, gvs1);
+          if (lane < kKeyTile / 8) block_scales_of(p, table, key0 + 8 * lane, r.kv_end, r.kvh, gks, gvs1);
         }
         for (int v = 0; v < 2 && !failed; ++v) {
           const uint32_t slot = g % SLOTS, use = g / SLOTS;
@@ -1007,7 +1028,7 @@ __global__ void __launch_bounds__(KV8 ? kTileThreads8 : kTileThreads, 1)
           } else if (h == first_reader(kt)) {
             wait_warp(bar(Lay::B_FULL + vslot), full_parity(kt, 1), failed);
             if (failed) break;
-            const int key0 = kt * kKeyTile;
+            const int key0 = (BSC ? r.kv_begin : 0) + kt * kKeyTile;
             if (key0 + kKeyTile > r.kv_end) {
               // rows of keys past kv_end may hold anything (even NaN): zero them in V
               const uint32_t sV = sRing + vslot * Lay::KV_BYTES;
@@ -1169,7 +1190,7 @@ __global__ void __launch_bounds__(KV8 ? kTileThreads8 : kTileThreads, 1)
       const int lim = row_valid ? cur.pos0 + qi + 1 : 0;  // keys j < lim are visible to this row
       float m_used = -INFINITY, l = 0.f;
       for (int kt = 0; kt < nk; ++kt) {
-        const int ck0 = kt * kKeyTile + part * PART_KEYS;  // this warp's first key of the range
+        const int ck0 = (BSC ? cur.kv_begin : 0) + kt * kKeyTile + part * PART_KEYS;  // this warp's first key of the range
         const uint32_t sp = t_lane + Tm::SP + part * PART_KEYS;
         wait_warp(bar(Lay::B_S + h), (phh + kt) & 1u, failed);
         if (failed) break;
@@ -1286,11 +1307,29 @@ __global__ void __launch_bounds__(KV8 ? kTileThreads8 : kTileThreads, 1)
         const float inv = lt > 0.f ? p.out_scale / lt : 0.f;
         bf16 *dst = p.out + static_cast<int64_t>(cur.row0 + (row_valid ? qi : 0)) * p.num_heads * D +
                     static_cast<int64_t>(cur.kvh * G + g) * D;
+        float *pdst = nullptr;  // the row's partial, for a part of the tile's keys
+        if constexpr (BSC) {
+          if (cur.slot >= 0) {
+            const int64_t prow = static_cast<int64_t>(cur.slot) * kPrefillTileRows + h * kHalfRows + r;
+            pdst = p.part_o + prow * D;
+            if (part == 0 && row_valid) p.part_lse[prow] = lt != 0.f ? m_used + __log2f(lt) : -INFINITY;
+          }
+        }
 #pragma unroll 1
         for (int ch = ch0; ch < ch1; ++ch) {
           uint32_t t[32];
           tmem_ld32_wait(t_lane + Tm::O + ch * 32, t);
-          if (row_valid) {
+          if (BSC && pdst) {
+            if (row_valid) {
+#pragma unroll
+              for (int c = 0; c < 8; ++c) {
+                if (32 * ch + 4 * c >= D) continue;
+                const float *f = reinterpret_cast<const float *>(&t[4 * c]);
+                *reinterpret_cast<float4 *>(pdst + ch * 32 + 4 * c) =
+                    make_float4(f[0] * inv, f[1] * inv, f[2] * inv, f[3] * inv);
+              }
+            }
+          } else if (row_valid) {
 #pragma unroll
             for (int c = 0; c < 4; ++c) {
               if (32 * ch + 8 * c >= D) continue;  // head_dim 80: the last 16 columns are padding
@@ -1302,6 +1341,9 @@ __global__ void __launch_bounds__(KV8 ? kTileThreads8 : kTileThreads, 1)
           }
         }
         tc_fence_before();  // O is overwritten by a later unit's first product
+      } else if (BSC && cur.slot >= 0 && part == 0 && row_valid) {
+        // the half sees none of this part's keys
+        p.part_lse[static_cast<int64_t>(cur.slot) * kPrefillTileRows + h * kHalfRows + r] = -INFINITY;
       }
       phh += nk;
       gvs += nkt_all;
@@ -1477,18 +1519,19 @@ __global__ void __launch_bounds__(kWideThreads, 1)
     r.stop = 1;
     if (!failed) {
       const volatile int *u = units + 8 * s;
-      r.b = u[0];
+      r.slot = u[0];
       r.row0 = u[1];
       r.npos = u[2];
       r.pos0 = u[3];
       r.kv_end = u[4];
       r.kvh = u[5];
       r.stop = u[6];
+      r.kv_begin = BSC ? u[7] : 0;
     }
     __syncwarp();
     if (lane == 0 && !failed) mbar_arrive(bar(Lay::B_UE + s));
   };
-  auto nranges = [&](const TileUnit &r) { return (r.kv_end + kKeyTile - 1) / kKeyTile; };
+  auto nranges = [&](const TileUnit &r) { return (r.kv_end - (BSC ? r.kv_begin : 0) + kKeyTile - 1) / kKeyTile; };
 
   if (warp == kTmaWarp) {
     // ---------------- producer ----------------
@@ -1501,7 +1544,7 @@ __global__ void __launch_bounds__(kWideThreads, 1)
       int u = 0;
       if (lane == 0) u = atomicAdd(p.tile_counter, 1);
       u = __shfl_sync(FULL, u, 0);
-      TileUnit r{0, 0, 0, 0, 0, 0, u >= total_units ? 1 : 0};
+      TileUnit r{0, 0, 0, 0, 0, 0, u >= total_units ? 1 : 0, 0, -1};
       if (!r.stop) {
         const int item = u / Hkv;
         r.kvh = u - item * Hkv;
@@ -1512,8 +1555,13 @@ __global__ void __launch_bounds__(kWideThreads, 1)
         r.npos = r0.z;
         r.pos0 = r0.w;
         r.kv_end = r1.y;
+        if constexpr (BSC) {
+          r.kv_begin = r1.x;
+          r.slot = r1.z >= 0 ? item * Hkv + r.kvh : -1;
+        }
         const bool sane = r.b >= 0 && r.b < p.num_seqs && r.npos >= 1 && r.npos <= POS && r.row0 >= 0 &&
-                          r.row0 + r.npos <= p.total_q && r.pos0 >= 0 && r.kv_end == r.pos0 + r.npos &&
+                          r.row0 + r.npos <= p.total_q && r.pos0 >= 0 &&
+                          (BSC ? part_sane(r, p, item) : r.kv_end == r.pos0 + r.npos) &&
                           r.kv_end <= static_cast<int64_t>(p.max_blocks_per_seq) * bs;
         if (!sane) {
           if (lane == 0) flag_error(p.status, PA_FLAG_LENGTHS);
@@ -1525,13 +1573,14 @@ __global__ void __launch_bounds__(kWideThreads, 1)
       if (failed) break;
       if (lane == 0) {
         volatile int *d = units + 8 * s;
-        d[0] = r.b;
+        d[0] = BSC ? r.slot : -1;
         d[1] = r.row0;
         d[2] = r.npos;
         d[3] = r.pos0;
         d[4] = r.kv_end;
         d[5] = r.kvh;
         d[6] = r.stop;
+        if (BSC) d[7] = r.kv_begin;
         mbar_arrive(bar(Lay::B_UF + s));
       }
       __syncwarp();
@@ -1549,10 +1598,11 @@ __global__ void __launch_bounds__(kWideThreads, 1)
       };
       const int nkt = nranges(r);
       for (int kt = 0; kt < nkt && !failed; ++kt) {
-        const int z = lane < nbk ? box_z(kt * kKeyTile + lane * box_rows, box_rows) : 0;
+        const int key0 = (BSC ? r.kv_begin : 0) + kt * kKeyTile;  // first key of the range
+        const int z = lane < nbk ? box_z(key0 + lane * box_rows, box_rows) : 0;
         float gks = 1.f, gvs1 = 1.f;  // block scales of 8-key group `lane` (1 past the last key)
         if constexpr (BSC) {
-          if (lane < kKeyTile / 8) block_scales_of(p, table, kt * kKeyTile + 8 * lane, r.kv_end, r.kvh, gks, gvs1);
+          if (lane < kKeyTile / 8) block_scales_of(p, table, key0 + 8 * lane, r.kv_end, r.kvh, gks, gvs1);
         }
         for (int v = 0; v < LPR && !failed; ++v) {
           const uint32_t slot = g % SLOTS, use = g / SLOTS;
@@ -1705,7 +1755,7 @@ __global__ void __launch_bounds__(kWideThreads, 1)
         wait_warp(bar(Lay::B_FULL + vs0), full_parity(kt, 2), failed);
         wait_warp(bar(Lay::B_FULL + vs1), full_parity(kt, 3), failed);
         if (failed) break;
-        const int key0 = kt * kKeyTile;
+        const int key0 = (BSC ? r.kv_begin : 0) + kt * kKeyTile;
         if (key0 + kKeyTile > r.kv_end) {
           // rows of keys past kv_end may hold anything (even NaN): zero them in both V units
           const int vr0 = r.kv_end - key0;
@@ -1844,7 +1894,7 @@ __global__ void __launch_bounds__(kWideThreads, 1)
       float m_used = -INFINITY, l = 0.f;
       for (int kt = 0; kt < nk; ++kt) {
         const uint32_t gr = ph + kt;
-        const int ck0 = kt * kKeyTile + part * 64;
+        const int ck0 = (BSC ? cur.kv_begin : 0) + kt * kKeyTile + part * 64;
         const uint32_t sp = tmem + lane_off + Tm::SP0 + (gr & 1u) * kKeyTile + part * 64;
         wait_warp(bar(Lay::B_S + (gr & 1u)), (gr >> 1) & 1u, failed);
         if (failed) break;
@@ -1940,11 +1990,28 @@ __global__ void __launch_bounds__(kWideThreads, 1)
         const float inv = lt > 0.f ? p.out_scale / lt : 0.f;
         bf16 *dst = p.out + static_cast<int64_t>(cur.row0 + (row_valid ? qi : 0)) * p.num_heads * D +
                     static_cast<int64_t>(cur.kvh * G + g) * D;
+        float *pdst = nullptr;  // the row's partial, for a part of the tile's keys
+        if constexpr (BSC) {
+          if (cur.slot >= 0) {
+            const int64_t prow = static_cast<int64_t>(cur.slot) * kPrefillTileRows128 + r;
+            pdst = p.part_o + prow * D;
+            if (part == 0 && row_valid) p.part_lse[prow] = lt != 0.f ? m_used + __log2f(lt) : -INFINITY;
+          }
+        }
 #pragma unroll 1
         for (int ch = part * 4; ch < part * 4 + 4; ++ch) {
           uint32_t t[32];
           tmem_ld32_wait(tmem + lane_off + Tm::O + ch * 32, t);
-          if (row_valid) {
+          if (BSC && pdst) {
+            if (row_valid) {
+#pragma unroll
+              for (int c = 0; c < 8; ++c) {
+                const float *f = reinterpret_cast<const float *>(&t[4 * c]);
+                *reinterpret_cast<float4 *>(pdst + ch * 32 + 4 * c) =
+                    make_float4(f[0] * inv, f[1] * inv, f[2] * inv, f[3] * inv);
+              }
+            }
+          } else if (row_valid) {
 #pragma unroll
             for (int c = 0; c < 4; ++c) {
               const float *f = reinterpret_cast<const float *>(&t[8 * c]);

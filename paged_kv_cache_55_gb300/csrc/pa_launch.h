@@ -129,12 +129,13 @@ cudaError_t launch_attention(const AttnLaunch &a, cudaStream_t stream, int *laun
 
 // Workspace of attention over 8-bit caches with block scales (attention_block.cu): byte offsets.
 struct BlockWorkspace {
-  size_t counts, nparts, first_full, rest, items, tiles, part_lse, part_o, total;
-  int32_t max_items;  // upper bound on decode work items (per KV head)
-  int32_t max_tiles;  // upper bound on prefill tiles (per KV head)
+  size_t counts, nparts, first_full, rest, items, tiles, part_lse, part_o, tile_lse, tile_o, total;
+  int32_t max_items;   // upper bound on decode work items (per KV head)
+  int32_t max_tiles;   // upper bound on prefill tiles or their parts (per KV head)
+  int32_t part_items;  // of these, how many may be parts of a split tile
 };
-bool block_workspace_layout(int32_t num_seqs, int32_t total_q, int32_t max_seq_len, int32_t num_heads,
-                            int32_t num_kv_heads, int32_t head_dim, BlockWorkspace &w);
+bool block_workspace_layout(int32_t num_seqs, int32_t total_q, int32_t max_query_len, int32_t max_seq_len,
+                            int32_t num_heads, int32_t num_kv_heads, int32_t head_dim, BlockWorkspace &w);
 // The same for caches with block scales (a.k_scales, a.v_scales).
 cudaError_t launch_block_attention(const AttnLaunch &a, cudaStream_t stream, int *launched);
 

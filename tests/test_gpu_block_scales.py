@@ -250,6 +250,13 @@ ATTENTION = {
                            head_dim=256),
     "sharp_g4_d128": dict(context_lens=[300, 900, 17], query_lens=[1, 2, 150], num_heads=8, num_kv_heads=2,
                           head_dim=128, q_scale=8.0),
+    "chunks_of_many_tiles": dict(context_lens=[100, 0, 300, 40, 5, 130], query_lens=[400] * 6, num_heads=32,
+                                 num_kv_heads=16, head_dim=64),
+    "one_chunk_long_context": dict(context_lens=[5000], query_lens=[40], num_heads=8, num_kv_heads=2, head_dim=128),
+    "one_chunk_long_context_d256": dict(context_lens=[3000], query_lens=[40], num_heads=4, num_kv_heads=1,
+                                        head_dim=256),
+    "chunk_whose_halves_end_apart": dict(context_lens=[100], query_lens=[700], num_heads=1, num_kv_heads=1,
+                                         head_dim=64),
     "scales_far_apart": dict(context_lens=[300, 900, 17, 400], query_lens=[1, 2, 150, 200], num_heads=8,
                              num_kv_heads=2, head_dim=128, v_exp=(-20, 4), k_exp=(-12, -5)),
     "scales_far_apart_d256": dict(context_lens=[300, 17, 400], query_lens=[1, 150, 200], num_heads=4, num_kv_heads=2,
@@ -309,6 +316,27 @@ def test_one_scale_everywhere_agrees_with_the_per_cache_call():
     torch.cuda.synchronize()
     diff = (out.float() - s.out.float()).abs()
     assert (diff <= 2.0 ** -7 * s.out.float().abs() + 2.0 ** -9).all()
+
+
+@pytest.mark.parametrize("lens", [([2000, 40], [1, 1]), ([700, 40], [40, 3])])
+def test_a_nan_reaches_only_its_own_rows(lens):
+    """A NaN value code of a visible key, a NaN scale, or a NaN query: NaN in the rows that see it (through
+    the split partials too), the other requests and KV heads untouched."""
+    s = Step(*lens, 4, 2, 64, seed=26, spread=0.3)
+    s.scatter()
+    s.attention()
+    torch.cuda.synchronize()
+    clean = s.out.clone()
+    s.d_vc[int(s.tables[0, 3]), 5, 1, 7] = 0x7F       # request 0, KV head 1 (query heads 2, 3), d 7
+    s.q[int(s.starts[1]), 0, 0] = float("nan")        # request 1's first row, query head 0
+    s.attention()
+    torch.cuda.synchronize()
+    n0 = int(s.starts[1])
+    assert s.out[:n0, 2:, 7].isnan().all() and s.out[n0, 0].isnan().all()
+    keep = torch.ones_like(s.out, dtype=torch.bool)
+    keep[:n0, 2:, 7] = False
+    keep[n0, 0] = False
+    assert torch.equal(s.out[keep], clean[keep])
 
 
 def test_one_long_request():
