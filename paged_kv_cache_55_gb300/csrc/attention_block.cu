@@ -932,12 +932,15 @@ __global__ void __launch_bounds__(NW * 32) block_merge_kernel(const MergeParams 
     const int4 r0 = ld_cg(p.tiles + 2 * item), r1 = ld_cg(p.tiles + 2 * item + 1);
     const int row0 = r0.y, npos = r0.z, parts = r1.w;
     constexpr int ROWS = prefill_tile_rows(D);
-    if (r1.z != 0 || parts <= 1 || item + parts > p.tile_items) return;  // the tile's first part speaks for it
+    // the CTAs of a part take its share of the tile's rows
+    const int part = r1.z, first = item - part;
+    if (parts <= 1 || part < 0 || part >= parts || first < 0 || first + parts > p.tile_items) return;
     if (row0 < 0 || npos < 1 || npos * G > ROWS || row0 + npos > p.total_q) return;
-    for (int row = rb * NW + warp; row < npos * G; row += kTileMergeCtas * NW) {
+    const int row_end = npos * G * (part + 1) / parts;
+    for (int row = npos * G * part / parts + rb * NW + warp; row < row_end; row += kTileMergeCtas * NW) {
       Merged<D> m;
       m.add(0, parts, lane, p.tile_lse, p.tile_o, [&](int k) {
-        return (static_cast<int64_t>(item + k) * p.num_kv_heads + kvh) * ROWS + row;
+        return (static_cast<int64_t>(first + k) * p.num_kv_heads + kvh) * ROWS + row;
       });
       m.template store<E>(p.out + static_cast<int64_t>(row0 + row / G) * p.num_heads * D +
                               static_cast<int64_t>(kvh * G + row % G) * D,
@@ -1127,7 +1130,8 @@ cudaError_t launch_typed(const AttnLaunch &a, const BlockWorkspace &w, cudaStrea
     tp.part_lse = reinterpret_cast<float *>(ws + w.tile_lse);
     tp.status = a.status;
     if (a.tile_start) cudaEventRecord(a.tile_start, stream);
-    err = launch_prefill_tiles<D, G, E, true, true>(kmap, vmap, vmap, tp, a.sm_count, stream);
+    err = a.block_size >= 16 ? launch_prefill_tiles<D, G, E, true, 16>(kmap, vmap, vmap, tp, a.sm_count, stream)
+                             : launch_prefill_tiles<D, G, E, true, 8>(kmap, vmap, vmap, tp, a.sm_count, stream);
     if (err != cudaSuccess) return err;
     if (a.tile_stop) cudaEventRecord(a.tile_stop, stream);
     ++*launched;

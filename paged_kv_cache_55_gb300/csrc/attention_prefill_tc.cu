@@ -74,8 +74,11 @@ constexpr int kParts = 2;        // softmax warps per TMEM lane quadrant and hal
 constexpr int kKeyTile = 128;    // keys per range (UMMA N of S, K of P V)
 constexpr int kMaxSlots = 8;     // K/V ring slots (as many as shared memory holds)
 constexpr int kUnitSlots = 2;    // published unit records
-// Block scales of a range, per 8-key group: K's scale and log2 of V's (8-bit caches with block scales).
-constexpr int kScaleSlotBytes = kKeyTile / 8 * 8;
+// Block scales of a range (8-bit caches with block scales; BSC is the group of
+// keys that shares a block, 16, or 8 for 8-token blocks): per group K's scale
+// times the softmax scale and log2 of V's, and for 16-key groups the inverse of
+// V's (16 bytes with padding; 8-key groups take the inverse again, 8 bytes).
+constexpr int kScaleSlotBytes = 128;
 constexpr int kScaleSlotsMax = kMaxSlots / 2 + 1;
 // Warp roles. The MMA warp is warp 0: its issue rate sets the tensor cores'
 // (they queue only a couple of products) and it shares a scheduler with
@@ -203,7 +206,8 @@ __device__ __forceinline__ void mma_ts(uint32_t d_tmem, uint32_t a_tmem, uint32_
       : "memory");
 }
 
-// Block scales of two neighbouring 8-key groups: (K scale, log2 V scale) of each.
+// Block scales of 16 keys: (K factor, log2 V scale, 1 / V scale, -) of a
+// 16-key group, or (K factor, log2 V scale) of two 8-key groups.
 __device__ __forceinline__ float4 ld_scales(uint32_t addr) {
   float4 v;
   asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];\n"
@@ -277,27 +281,34 @@ __device__ __forceinline__ float masked_max32(const uint32_t (&s)[32], int ck0, 
   return m;
 }
 
-// Row maximum of 32 scores under block scales: s * (sl2 * ks) + lv of each
-// 8-key group (scale pairs at shared address sc), as separately rounded
-// operations. ks and sl2 are positive, so a group's largest raw score gives
-// its largest scaled one.
-__device__ __forceinline__ float scaled_max32(const uint32_t (&s)[32], int ck0, int lim, float sl2, uint32_t sc) {
-  const float4 c01 = ld_scales(sc), c23 = ld_scales(sc + 16);
-  const float ks[4] = {c01.x, c01.z, c23.x, c23.z}, lv[4] = {c01.y, c01.w, c23.y, c23.w};
+// Row maximum of 32 scores under block scales (at shared address sc): s * (rowf * kf) + lv per group, as separately rounded operations. kf
+// and rowf are positive, so a group's largest raw score gives its largest
+// scaled one.
+template <int GRP>
+__device__ __forceinline__ float scaled_max32(const uint32_t (&s)[32], int ck0, int lim, float rowf, uint32_t sc) {
   float m = -INFINITY;
+  float4 v;
 #pragma unroll
-  for (int g = 0; g < 4; ++g) {
+  for (int g = 0; g < 32 / GRP; ++g) {
+    constexpr int PER16 = 16 / GRP;  // groups per 16 keys
+    if (g % PER16 == 0) v = ld_scales(sc + 16 * (g / PER16));
+    const float kf = g % PER16 == 0 ? v.x : v.z, lv = g % PER16 == 0 ? v.y : v.w;
     float t;
     if (ck0 + 32 <= lim) {
-      t = max3(max3(__uint_as_float(s[8 * g]), __uint_as_float(s[8 * g + 1]), __uint_as_float(s[8 * g + 2])),
-               max3(__uint_as_float(s[8 * g + 3]), __uint_as_float(s[8 * g + 4]), __uint_as_float(s[8 * g + 5])),
-               fmaxf(__uint_as_float(s[8 * g + 6]), __uint_as_float(s[8 * g + 7])));
+      t = max3(__uint_as_float(s[GRP * g]), __uint_as_float(s[GRP * g + 1]), __uint_as_float(s[GRP * g + 2]));
+      float u = max3(__uint_as_float(s[GRP * g + 3]), __uint_as_float(s[GRP * g + 4]), __uint_as_float(s[GRP * g + 5]));
+#pragma unroll
+      for (int i = 6; i < GRP; i += 4) {
+        t = max3(t, __uint_as_float(s[GRP * g + i]), __uint_as_float(s[GRP * g + i + 1]));
+        if (i + 3 < GRP) u = max3(u, __uint_as_float(s[GRP * g + i + 2]), __uint_as_float(s[GRP * g + i + 3]));
+      }
+      t = fmaxf(t, u);
     } else {
       t = -INFINITY;
 #pragma unroll
-      for (int i = 0; i < 8; ++i) t = ck0 + 8 * g + i < lim ? fmaxf(t, __uint_as_float(s[8 * g + i])) : t;
+      for (int i = 0; i < GRP; ++i) t = ck0 + GRP * g + i < lim ? fmaxf(t, __uint_as_float(s[GRP * g + i])) : t;
     }
-    m = fmaxf(m, __fadd_rn(__fmul_rn(t, __fmul_rn(sl2, ks[g])), lv[g]));
+    m = fmaxf(m, __fadd_rn(__fmul_rn(t, __fmul_rn(rowf, kf)), lv));
   }
   return m;
 }
@@ -357,24 +368,23 @@ __device__ __forceinline__ void probs16_store(const uint32_t *s, int k0, int lim
   if (SPLIT) tmem_st8u(col + 8, lv);
 }
 
-// The same for 16 keys under block scales, one fp16 P per key: the first and
-// the last eight keys have scale pairs (K scale ks, lv = log2 V scale) at
-// shared address sc. P' = 2^(s * sl2 * ks + lv - ms) carries the V scale, so O
-// accumulates P' times codes; the row sum takes P' / 2^lv.
-template <bool EXACT>
-__device__ __forceinline__ void probs16_scaled_store(const uint32_t *s, int k0, int lim, float sl2, float ms,
-                                                     float &sum, uint32_t col, uint32_t sc) {
+// The same for 16 keys under block scales `c`, one fp16 P per key:
+// P' = 2^(s * kf + lv - ms) carries the V scale 2^lv, so O accumulates P' times
+// codes; the row sum takes P' / 2^lv. EXACT rows also apply the row's factor
+// (1 otherwise).
+template <int GRP, bool EXACT>
+__device__ __forceinline__ void probs16_scaled_store(const uint32_t *s, int k0, int lim, float rowf, float ms,
+                                                     float &sum, uint32_t col, const float4 &c) {
   const bool full = k0 + 16 <= lim;
-  const float4 c = ld_scales(sc);
-  const float f[2] = {__fmul_rn(sl2, c.x), __fmul_rn(sl2, c.z)}, lv[2] = {c.y, c.w};
   uint32_t hv[8];
 #pragma unroll
-  for (int g = 0; g < 2; ++g) {
-    const float add = lv[g] - ms;
+  for (int g = 0; g < 16 / GRP; ++g) {
+    const float kf = g == 0 ? c.x : c.z, lv = g == 0 ? c.y : c.w;
+    const float f = EXACT ? __fmul_rn(rowf, kf) : kf, add = lv - ms;
     float acc0 = 0.f, acc1 = 0.f;
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const int i = 4 * g + j;
+    for (int j = 0; j < GRP / 2; ++j) {
+      const int i = GRP / 2 * g + j;
       float x0 = __uint_as_float(s[2 * i]), x1 = __uint_as_float(s[2 * i + 1]);
       if (!full) {
         x0 = k0 + 2 * i < lim ? x0 : -INFINITY;
@@ -382,16 +392,16 @@ __device__ __forceinline__ void probs16_scaled_store(const uint32_t *s, int k0, 
       }
       float e0, e1;
       if (EXACT) {
-        e0 = __fsub_rn(__fadd_rn(__fmul_rn(x0, f[g]), lv[g]), ms);
-        e1 = __fsub_rn(__fadd_rn(__fmul_rn(x1, f[g]), lv[g]), ms);
+        e0 = __fsub_rn(__fadd_rn(__fmul_rn(x0, f), lv), ms);
+        e1 = __fsub_rn(__fadd_rn(__fmul_rn(x1, f), lv), ms);
       } else {
-        fma2(e0, e1, x0, x1, f[g], f[g], add, add);
+        fma2(e0, e1, x0, x1, f, f, add, add);
       }
       const float p0 = ex2_approx(e0), p1 = ex2_approx(e1);
       add2(acc0, acc1, acc0, acc1, p0, p1);
       hv[i] = ElemFp16::pack(p0, p1);
     }
-    sum = fmaf(acc0 + acc1, ex2_approx(-lv[g]), sum);
+    sum = fmaf(acc0 + acc1, GRP == 16 ? c.z : ex2_approx(-lv), sum);
   }
   tmem_st8u(col, hv);
 }
@@ -441,7 +451,7 @@ __device__ __forceinline__ void tmem_ld32x2_wait(uint32_t taddr, uint32_t (&a)[3
       : "memory");
 }
 
-// Block scales of the 8-key group that starts at `key` (this KV head); left as
+// Block scales of the group that starts at `key` (this KV head); left as
 // they are past the last key or for a block id out of range. p.k_scales and
 // p.v_scales may have been written shortly before: not an invariant load.
 __device__ __forceinline__ void block_scales_of(const TileParams &p, const int32_t *table, int key, int kv_end, int kvh,
@@ -453,8 +463,15 @@ __device__ __forceinline__ void block_scales_of(const TileParams &p, const int32
   ks = ld_cg(p.k_scales + at);
   vs = ld_cg(p.v_scales + at);
 }
-__device__ __forceinline__ void st_scales(uint32_t addr, float ks, float lv) {
-  asm volatile("st.shared.v2.f32 [%0], {%1, %2};\n" ::"r"(addr), "f"(ks), "f"(lv) : "memory");
+template <int GRP>
+__device__ __forceinline__ void st_scales(uint32_t slot, int group, float kf, float vs) {
+  const float lv = __log2f(vs);
+  if (GRP == 16)
+    asm volatile("st.shared.v4.f32 [%0], {%1, %2, %3, %3};\n" ::"r"(slot + 16 * group), "f"(kf), "f"(lv),
+                 "f"(__fdividef(1.f, vs))
+                 : "memory");
+  else
+    asm volatile("st.shared.v2.f32 [%0], {%1, %2};\n" ::"r"(slot + 8 * group), "f"(kf), "f"(lv) : "memory");
 }
 
 // A published unit: a tile of one request and one KV head, or the end of the stream.
@@ -557,10 +574,10 @@ __device__ __forceinline__ void vrange_back_to_bf16(uint32_t sV, int c0, int nva
 // pair for that range. Either way the rows past the unit's last key are
 // zeroed.
 //
-// With block scales (BSC) the producer also stages each range's scales, one
-// pair (K scale, log2 V scale) per 8-key group, which the softmax warps fold
-// into the exponents as the decode kernel does (probs16_scaled_store).
-template <int D, int G, typename E, bool KV8, bool BSC>
+// With block scales (BSC, the keys of a group) the producer also stages each
+// range's scales, which the softmax warps fold into the exponents as the decode
+// kernel does (probs16_scaled_store).
+template <int D, int G, typename E, bool KV8, int BSC>
 // Twenty warps (two of them idle over fp16 caches), one CTA per SM.
 __global__ void __launch_bounds__(KV8 ? kTileThreads8 : kTileThreads, 1)
     prefill_tile_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap,
@@ -724,7 +741,7 @@ __global__ void __launch_bounds__(KV8 ? kTileThreads8 : kTileThreads, 1)
         r.npos = r0.z;
         r.pos0 = r0.w;
         r.kv_end = r1.y;
-        if constexpr (BSC) {
+        if constexpr (BSC != 0) {
           r.kv_begin = r1.x;
           r.slot = r1.z >= 0 ? item * Hkv + r.kvh : -1;
         }
@@ -776,19 +793,19 @@ __global__ void __launch_bounds__(KV8 ? kTileThreads8 : kTileThreads, 1)
         const int key0 = (BSC ? r.kv_begin : 0) + kt * kKeyTile;  // first key of the range
         const int zk = lane < nbk ? box_z(key0 + lane * box_rows, box_rows) : 0;
         const int zv = VBLK ? (lane < nbv ? box_z(key0 + lane * bs, bs) : 0) : zk;
-        float gks = 1.f, gvs1 = 1.f;  // block scales of 8-key group `lane` (1 past the last key)
-        if constexpr (BSC) {
-          if (lane < kKeyTile / 8) block_scales_of(p, table, key0 + 8 * lane, r.kv_end, r.kvh, gks, gvs1);
+        float gks = 1.f, gvs1 = 1.f;  // block scales of group `lane` (1 past the last key)
+        if constexpr (BSC != 0) {
+          if (lane < kKeyTile / BSC) block_scales_of(p, table, key0 + BSC * lane, r.kv_end, r.kvh, gks, gvs1);
         }
         for (int v = 0; v < 2 && !failed; ++v) {
           const uint32_t slot = g % SLOTS, use = g / SLOTS;
           if (use > 0) wait_warp(bar(Lay::B_EMPTY + slot), (use - 1) & 1u, failed);
           if (failed) break;
-          if constexpr (BSC) {
+          if constexpr (BSC != 0) {
             if (v == 0) {
               const uint32_t fi = (g / 2) % Lay::SCALE_SLOTS;
-              if (lane < kKeyTile / 8)
-                st_scales(base + Lay::SC_OFF + fi * kScaleSlotBytes + 8 * lane, gks, __log2f(gvs1));
+              if (lane < kKeyTile / BSC)
+                st_scales<BSC>(base + Lay::SC_OFF + fi * kScaleSlotBytes, lane, gks * p.scale_log2, gvs1);
               __syncwarp();
               if (lane == 0) mbar_arrive(bar(Lay::B_SC + fi));  // release: the range's scales
             }
@@ -1139,7 +1156,7 @@ __global__ void __launch_bounds__(KV8 ? kTileThreads8 : kTileThreads, 1)
         }
         return w;
       };
-      float sl2 = p.scale_log2;  // > 0: the max of raw scores gives the max of scaled ones
+      float sl2 = BSC ? 1.f : p.scale_log2;  // > 0: the max of raw scores gives the max of scaled ones
       float qmul = 1.f;
       if constexpr (KV8 && std::is_same<E, ElemBf16>::value) {
         // bf16 rows over 8-bit caches: 2^-e, e > 0 only when the row's largest |q| reaches 2^15
@@ -1194,6 +1211,14 @@ __global__ void __launch_bounds__(KV8 ? kTileThreads8 : kTileThreads, 1)
         const uint32_t sp = t_lane + Tm::SP + part * PART_KEYS;
         wait_warp(bar(Lay::B_S + h), (phh + kt) & 1u, failed);
         if (failed) break;
+        uint32_t sc = 0;  // block scales: this warp's keys of the range
+        if constexpr (BSC != 0) {
+          // (already there: they were written before the K that S came from)
+          const uint32_t gv = gvs + kt, fi = gv % Lay::SCALE_SLOTS;
+          wait_warp(bar(Lay::B_SC + fi), (gv / Lay::SCALE_SLOTS) & 1u, failed);
+          if (failed) break;
+          sc = base + Lay::SC_OFF + fi * kScaleSlotBytes + part * (kScaleSlotBytes / kParts);
+        }
         tc_fence_after();
         uint32_t s0[32], s1[32];
         tmem_ld32x2_wait(sp, s0, s1);
@@ -1201,14 +1226,10 @@ __global__ void __launch_bounds__(KV8 ? kTileThreads8 : kTileThreads, 1)
         // m_used, as separately rounded operations (no contraction into one
         // fused multiply-add): the exponents below are bounded by exactly this
         // difference. The other warp reads its scores before either writes P.
-        uint32_t sc = 0;  // block scales: this warp's groups of the range
         float mx;
-        if constexpr (BSC) {
-          const uint32_t gv = gvs + kt, fi = gv % Lay::SCALE_SLOTS;
-          wait_warp(bar(Lay::B_SC + fi), (gv / Lay::SCALE_SLOTS) & 1u, failed);
-          if (failed) break;
-          sc = base + Lay::SC_OFF + fi * kScaleSlotBytes + part * (PART_KEYS / 8) * 8;
-          mx = fmaxf(scaled_max32(s0, ck0, lim, sl2, sc), scaled_max32(s1, ck0 + 32, lim, sl2, sc + 32));
+        if constexpr (BSC != 0) {
+          mx = scaled_max32<BSC>(s0, ck0, lim, sl2, sc);
+          mx = fmaxf(mx, scaled_max32<BSC>(s1, ck0 + 32, lim, sl2, sc + 32));
         } else {
           mx = fmaxf(masked_max32(s0, ck0, lim), masked_max32(s1, ck0 + 32, lim));
         }
@@ -1223,7 +1244,8 @@ __global__ void __launch_bounds__(KV8 ? kTileThreads8 : kTileThreads, 1)
         }
         const float ms = m_used == -INFINITY ? 0.f : m_used;
         float sum = 0.f;
-        const bool exact = __any_sync(FULL, fabsf(ms) > 4096.f);
+        // (block scales: sl2 is the row's factor, 1 unless its q was scaled)
+        const bool exact = __any_sync(FULL, fabsf(ms) > 4096.f || (BSC != 0 && sl2 != 1.f));
         bool vpair = false;  // V(kt) kept bf16 (bf16 caches only): P as a hi + lo pair
         if constexpr (VCONV) {
           const uint32_t gv = gvs + kt, fi = gv % kMaxSlots;
@@ -1239,19 +1261,22 @@ __global__ void __launch_bounds__(KV8 ? kTileThreads8 : kTileThreads, 1)
         // P of step ks (8 columns at 8 ks) covers only scores read by
         // earlier steps. Rare cases stay out of the loop (inside it, as a
         // branch per step, they cost 2 %).
-        if constexpr (BSC) {
+        if constexpr (BSC != 0) {
           if (exact) {
+#pragma unroll 1
             for (int ks = 0; ks < PART_KEYS / 16; ++ks) {
+              const float4 c = ld_scales(sc + 16 * ks);
               uint32_t t[16];
               tmem_ld16_wait(sp + 16 * ks, t);
-              probs16_scaled_store<true>(t, ck0 + 16 * ks, lim, sl2, ms, sum, sp + 8 * ks, sc + 16 * ks);
+              probs16_scaled_store<BSC, true>(t, ck0 + 16 * ks, lim, sl2, ms, sum, sp + 8 * ks, c);
             }
           } else {
 #pragma unroll 2
             for (int ks = 0; ks < PART_KEYS / 16; ++ks) {
+              const float4 c = ld_scales(sc + 16 * ks);
               uint32_t t[16];
               tmem_ld16_wait(sp + 16 * ks, t);
-              probs16_scaled_store<false>(t, ck0 + 16 * ks, lim, sl2, ms, sum, sp + 8 * ks, sc + 16 * ks);
+              probs16_scaled_store<BSC, false>(t, ck0 + 16 * ks, lim, sl2, ms, sum, sp + 8 * ks, c);
             }
           }
         } else if (vpair) {
@@ -1308,7 +1333,7 @@ __global__ void __launch_bounds__(KV8 ? kTileThreads8 : kTileThreads, 1)
         bf16 *dst = p.out + static_cast<int64_t>(cur.row0 + (row_valid ? qi : 0)) * p.num_heads * D +
                     static_cast<int64_t>(cur.kvh * G + g) * D;
         float *pdst = nullptr;  // the row's partial, for a part of the tile's keys
-        if constexpr (BSC) {
+        if constexpr (BSC != 0) {
           if (cur.slot >= 0) {
             const int64_t prow = static_cast<int64_t>(cur.slot) * kPrefillTileRows + h * kHalfRows + r;
             pdst = p.part_o + prow * D;
@@ -1429,7 +1454,7 @@ struct WideLayout {
 static_assert(WideLayout::SLOTS == 5, "two scale slots");
 static_assert(WideLayout::BYTES <= 227 * 1024, "shared memory of one CTA");
 
-template <int G, typename E, bool KV8, bool BSC>
+template <int G, typename E, bool KV8, int BSC>
 __global__ void __launch_bounds__(kWideThreads, 1)
     prefill_tile_wide_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap,
                              const TileParams p) {
@@ -1555,7 +1580,7 @@ __global__ void __launch_bounds__(kWideThreads, 1)
         r.npos = r0.z;
         r.pos0 = r0.w;
         r.kv_end = r1.y;
-        if constexpr (BSC) {
+        if constexpr (BSC != 0) {
           r.kv_begin = r1.x;
           r.slot = r1.z >= 0 ? item * Hkv + r.kvh : -1;
         }
@@ -1600,19 +1625,19 @@ __global__ void __launch_bounds__(kWideThreads, 1)
       for (int kt = 0; kt < nkt && !failed; ++kt) {
         const int key0 = (BSC ? r.kv_begin : 0) + kt * kKeyTile;  // first key of the range
         const int z = lane < nbk ? box_z(key0 + lane * box_rows, box_rows) : 0;
-        float gks = 1.f, gvs1 = 1.f;  // block scales of 8-key group `lane` (1 past the last key)
-        if constexpr (BSC) {
-          if (lane < kKeyTile / 8) block_scales_of(p, table, key0 + 8 * lane, r.kv_end, r.kvh, gks, gvs1);
+        float gks = 1.f, gvs1 = 1.f;  // block scales of group `lane` (1 past the last key)
+        if constexpr (BSC != 0) {
+          if (lane < kKeyTile / BSC) block_scales_of(p, table, key0 + BSC * lane, r.kv_end, r.kvh, gks, gvs1);
         }
         for (int v = 0; v < LPR && !failed; ++v) {
           const uint32_t slot = g % SLOTS, use = g / SLOTS;
           if (use > 0) wait_warp(bar(Lay::B_EMPTY + slot), (use - 1) & 1u, failed);
           if (failed) break;
-          if constexpr (BSC) {
+          if constexpr (BSC != 0) {
             if (v == 0) {
               const uint32_t fi = (g / LPR) % Lay::SCALE_SLOTS;
-              if (lane < kKeyTile / 8)
-                st_scales(base + Lay::SC_OFF + fi * kScaleSlotBytes + 8 * lane, gks, __log2f(gvs1));
+              if (lane < kKeyTile / BSC)
+                st_scales<BSC>(base + Lay::SC_OFF + fi * kScaleSlotBytes, lane, gks * p.scale_log2, gvs1);
               __syncwarp();
               if (lane == 0) mbar_arrive(bar(Lay::B_SC + fi));  // release: the range's scales
             }
@@ -1845,7 +1870,7 @@ __global__ void __launch_bounds__(kWideThreads, 1)
         }
         return w;
       };
-      float sl2 = p.scale_log2;
+      float sl2 = BSC ? 1.f : p.scale_log2;
       float qmul = 1.f;
       if constexpr (KV8 && std::is_same<E, ElemBf16>::value) {
         float amax = 0.f;
@@ -1901,14 +1926,15 @@ __global__ void __launch_bounds__(kWideThreads, 1)
         tc_fence_after();
         uint32_t s0[32], s1[32];
         tmem_ld32x2_wait(sp, s0, s1);
-        uint32_t sc = 0;  // block scales: this warp's groups of the range
+        uint32_t sc = 0;  // block scales: this warp's keys of the range
         float mx;
-        if constexpr (BSC) {
+        if constexpr (BSC != 0) {
           const uint32_t fi = gr % Lay::SCALE_SLOTS;
           wait_warp(bar(Lay::B_SC + fi), (gr / Lay::SCALE_SLOTS) & 1u, failed);
           if (failed) break;
           sc = base + Lay::SC_OFF + fi * kScaleSlotBytes + part * 64;
-          mx = fmaxf(scaled_max32(s0, ck0, lim, sl2, sc), scaled_max32(s1, ck0 + 32, lim, sl2, sc + 32));
+          mx = scaled_max32<BSC>(s0, ck0, lim, sl2, sc);
+          mx = fmaxf(mx, scaled_max32<BSC>(s1, ck0 + 32, lim, sl2, sc + 32));
         } else {
           mx = fmaxf(masked_max32(s0, ck0, lim), masked_max32(s1, ck0 + 32, lim));
         }
@@ -1924,16 +1950,17 @@ __global__ void __launch_bounds__(kWideThreads, 1)
         const float ms = m_used == -INFINITY ? 0.f : m_used;
         float sum = 0.f;
         constexpr uint32_t PSTEP = SPLIT ? 16 : 8;
-        if constexpr (BSC) {
-          const bool exact = __any_sync(FULL, fabsf(ms) > 4096.f);
+        if constexpr (BSC != 0) {
+          const bool exact = __any_sync(FULL, fabsf(ms) > 4096.f || sl2 != 1.f);
 #pragma unroll 1
           for (int ks = 0; ks < 4; ++ks) {
+            const float4 c = ld_scales(sc + 16 * ks);
             uint32_t t[16];
             tmem_ld16_wait(sp + 16 * ks, t);
             if (exact)
-              probs16_scaled_store<true>(t, ck0 + 16 * ks, lim, sl2, ms, sum, sp + 8 * ks, sc + 16 * ks);
+              probs16_scaled_store<BSC, true>(t, ck0 + 16 * ks, lim, sl2, ms, sum, sp + 8 * ks, c);
             else
-              probs16_scaled_store<false>(t, ck0 + 16 * ks, lim, sl2, ms, sum, sp + 8 * ks, sc + 16 * ks);
+              probs16_scaled_store<BSC, false>(t, ck0 + 16 * ks, lim, sl2, ms, sum, sp + 8 * ks, c);
           }
         } else {
         if (__any_sync(FULL, fabsf(ms) > 4096.f)) {
@@ -1991,7 +2018,7 @@ __global__ void __launch_bounds__(kWideThreads, 1)
         bf16 *dst = p.out + static_cast<int64_t>(cur.row0 + (row_valid ? qi : 0)) * p.num_heads * D +
                     static_cast<int64_t>(cur.kvh * G + g) * D;
         float *pdst = nullptr;  // the row's partial, for a part of the tile's keys
-        if constexpr (BSC) {
+        if constexpr (BSC != 0) {
           if (cur.slot >= 0) {
             const int64_t prow = static_cast<int64_t>(cur.slot) * kPrefillTileRows128 + r;
             pdst = p.part_o + prow * D;
@@ -2047,7 +2074,7 @@ __global__ void __launch_bounds__(kWideThreads, 1)
   if (warp == 0) tmem_dealloc(tmem, kTmemCols);
 }
 
-template <int D, int G, typename E, bool KV8, bool BSC>
+template <int D, int G, typename E, bool KV8, int BSC>
 cudaError_t launch_prefill_tiles(const CUtensorMap &kmap, const CUtensorMap &vmap, const CUtensorMap &vmapb,
                                  const TileParams &tp, int sm_count, cudaStream_t stream) {
   if constexpr (D == kWideD) {
@@ -2084,12 +2111,14 @@ cudaError_t launch_prefill_tiles(const CUtensorMap &kmap, const CUtensorMap &vma
                                                                 const CUtensorMap &, const TileParams &, int, \
                                                                 cudaStream_t);
 #define PA_TILE_INST(DD, GG)                                                                              \
-  PA_TILE_INST1(DD, GG, ElemBf16, false, false)                                                           \
-  PA_TILE_INST1(DD, GG, ElemFp16, false, false)                                                           \
-  PA_TILE_INST1(DD, GG, ElemBf16, true, false)                                                            \
-  PA_TILE_INST1(DD, GG, ElemFp16, true, false)                                                            \
-  PA_TILE_INST1(DD, GG, ElemBf16, true, true)                                                             \
-  PA_TILE_INST1(DD, GG, ElemFp16, true, true)
+  PA_TILE_INST1(DD, GG, ElemBf16, false, 0)                                                           \
+  PA_TILE_INST1(DD, GG, ElemFp16, false, 0)                                                           \
+  PA_TILE_INST1(DD, GG, ElemBf16, true, 0)                                                            \
+  PA_TILE_INST1(DD, GG, ElemFp16, true, 0)                                                            \
+  PA_TILE_INST1(DD, GG, ElemBf16, true, 8)                                                                \
+  PA_TILE_INST1(DD, GG, ElemFp16, true, 8)                                                                \
+  PA_TILE_INST1(DD, GG, ElemBf16, true, 16)                                                               \
+  PA_TILE_INST1(DD, GG, ElemFp16, true, 16)
 PA_TILE_INST(128, 1)
 PA_TILE_INST(128, 2)
 PA_TILE_INST(128, 4)
