@@ -1,6 +1,6 @@
 // Attention over 8-bit caches with a scale per (block, KV head): planning,
 // split-KV decode and the log-sum-exp merge. Chunked-prefill requests go to
-// the tensor-core tiles of attention_prefill_tc.cu.
+// the tensor-core tiles of attention_block_prefill.cu.
 //
 // The mathematics. With x_j = scale q.Kc_j ks_j log2 e + log2 vs_j (ks_j, vs_j
 // the scales of key j's block) and any reference m,
@@ -1104,7 +1104,7 @@ cudaError_t launch_typed(const AttnLaunch &a, const BlockWorkspace &w, cudaStrea
   if (a.ev_stop) cudaEventRecord(a.ev_stop, stream);
 
   if (tiles_follow) {  // some request may be a prefill chunk
-    TileParams tp;
+    BlockTileParams tp;
     tp.q = dp.q;
     tp.q_stride = a.q_stride;
     tp.block_tables = a.block_tables;
@@ -1130,8 +1130,7 @@ cudaError_t launch_typed(const AttnLaunch &a, const BlockWorkspace &w, cudaStrea
     tp.part_lse = reinterpret_cast<float *>(ws + w.tile_lse);
     tp.status = a.status;
     if (a.tile_start) cudaEventRecord(a.tile_start, stream);
-    err = a.block_size >= 16 ? launch_prefill_tiles<D, G, E, true, 16>(kmap, vmap, vmap, tp, a.sm_count, stream)
-                             : launch_prefill_tiles<D, G, E, true, 8>(kmap, vmap, vmap, tp, a.sm_count, stream);
+    err = launch_block_tiles<D, G, E>(kmap, vmap, tp, a.sm_count, stream);
     if (err != cudaSuccess) return err;
     if (a.tile_stop) cudaEventRecord(a.tile_stop, stream);
     ++*launched;

@@ -40,28 +40,33 @@ struct TileParams {
   int32_t num_seqs;
   int32_t total_q;
   int32_t max_tiles;
-  const float *k_scales = nullptr;  // 8-bit caches with block scales: [num_blocks][Hkv]
-  const float *v_scales = nullptr;
-  // block scales: tiles may be split over their keys. Records {b, first query
-  // token, positions, absolute position of the first}, {key begin, key end,
-  // part (-1: the whole tile), parts}; the rows of a part of item i < max_part_items
-  // and KV head h go to slot i * Hkv + h of tile-rows rows (normalised outputs,
-  // fp32, and their log2-sum-exp).
-  int32_t max_part_items = 0;
-  float *part_o = nullptr;    // [slots][tile rows][D]
-  float *part_lse = nullptr;  // [slots][tile rows]
   unsigned int *status;
 };
 
 // Enqueue the tensor-core prefill-tile kernel (PDL launch) on `stream`; E is
 // the element type of q and out (ElemBf16 or ElemFp16); KV8: the caches hold
 // 8-bit E4M3 codes (the maps then have one-byte elements and boxes of
-// min(block_size, 32) rows of head_dim codes); BSC: with a scale per (block,
-// KV head) instead of one per cache, 16 for blocks of 16 or more tokens, else 8.
+// min(block_size, 32) rows of head_dim codes).
 // vmapb: at head_dim 128 over 16-bit caches, the value cache as whole-block
 // boxes (block_size rows x both 64-element atoms; unused otherwise).
-template <int D, int G, typename E, bool KV8, int BSC = 0>
+template <int D, int G, typename E, bool KV8>
 cudaError_t launch_prefill_tiles(const CUtensorMap &kmap, const CUtensorMap &vmap, const CUtensorMap &vmapb,
                                  const TileParams &tp, int sm_count, cudaStream_t stream);
+
+// The same over 8-bit caches with a scale per (block, KV head)
+// (attention_block_prefill.cu). Tiles may be split over their keys: records {b,
+// first query token, positions, absolute position of the first}, {key begin, key
+// end, part (-1: the whole tile), parts}; the rows of a part of item i <
+// max_part_items and KV head h go to slot i * Hkv + h of tile-rows rows
+// (normalised outputs, fp32, and their log2-sum-exp).
+struct BlockTileParams : TileParams {
+  const float *k_scales, *v_scales;  // [num_blocks][Hkv]
+  int32_t max_part_items;
+  float *part_o;    // [slots][tile rows][D]
+  float *part_lse;  // [slots][tile rows]
+};
+template <int D, int G, typename E>
+cudaError_t launch_block_tiles(const CUtensorMap &kmap, const CUtensorMap &vmap, const BlockTileParams &tp, int sm_count,
+                               cudaStream_t stream);
 
 }  // namespace pa

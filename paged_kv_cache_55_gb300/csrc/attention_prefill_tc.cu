@@ -63,263 +63,9 @@
 // file (S and O of two halves would not fit the 512 TMEM columns).
 #include <type_traits>
 
-#include "attention_internal.cuh"
+#include "attention_tile.cuh"
 
 namespace pa {
-
-constexpr int kHalfRows = 128;  // UMMA M: rows per half
-constexpr int kHalves = kPrefillTileRows / kHalfRows;
-static_assert(kHalves == 2, "the pipeline interleaves exactly two halves");
-constexpr int kParts = 2;        // softmax warps per TMEM lane quadrant and half (64 keys of a range each)
-constexpr int kKeyTile = 128;    // keys per range (UMMA N of S, K of P V)
-constexpr int kMaxSlots = 8;     // K/V ring slots (as many as shared memory holds)
-constexpr int kUnitSlots = 2;    // published unit records
-// Block scales of a range (8-bit caches with block scales; BSC is the group of
-// keys that shares a block, 16, or 8 for 8-token blocks): per group K's scale
-// times the softmax scale and log2 of V's, and for 16-key groups the inverse of
-// V's (16 bytes with padding; 8-key groups take the inverse again, 8 bytes).
-constexpr int kScaleSlotBytes = 128;
-constexpr int kScaleSlotsMax = kMaxSlots / 2 + 1;
-// Warp roles. The MMA warp is warp 0: its issue rate sets the tensor cores'
-// (they queue only a couple of products) and it shares a scheduler with
-// softmax warps; the schedulers favour lower-numbered warps when several are
-// ready. Warp 1 loads K/V; warps 2 and 3 widen 8-bit codes (idle otherwise);
-// warps 4 .. 19 run the softmax (warp % 4 is their TMEM lane quadrant).
-constexpr int kSoftmaxWarps = 4 * kHalves * kParts, kMmaWarp = 0, kTmaWarp = 1, kSoftmaxWarp0 = 4;
-constexpr int kTileThreads = 32 * (kSoftmaxWarp0 + kSoftmaxWarps);
-// 8-bit caches: two more warps widen each staged range to fp16 in place.
-constexpr int kConvWarp = 2, kConvWarps = 2;
-constexpr int kTileThreads8 = kTileThreads;
-constexpr int kRawBoxRows = 32;  // 8-bit boxes: min(block_size, 32) rows
-constexpr uint64_t kTcWaitTimeoutNs = 2000000000;
-constexpr uint32_t kTmemCols = 512;
-
-// Tensor memory columns of half A: the score buffer SP [0, 128) and O
-// [128, 128 + D); half B's are the same plus HALF. SP holds S (fp32, column
-// = key) and then P. With P as a bf16 hi + lo pair, the 16 keys of UMMA K
-// step k occupy columns [16k, 16k + 16) (8 columns of hi pairs, then 8 of lo
-// pairs); with one 16-bit P per key, K step k occupies 8 columns at 8k for
-// k < 4 and at 8k + 32 for k >= 4, so that each softmax warp's probabilities
-// stay inside the 64 score columns it reads (the other warp of its row may
-// still be reading its own).
-template <int D>
-struct TcTmem {
-  static constexpr uint32_t SP = 0, O = kKeyTile;
-  static constexpr uint32_t HALF = kTmemCols / kHalves;
-  static_assert(O + D <= HALF, "a half's columns must fit its share of TMEM");
-};
-
-template <int D>
-struct TcLayout {
-  // 64-element swizzle atoms along D; head_dim 80 or 96 is padded to two, the
-  // columns past it zero-filled by TMA (K, V) and never read (Q)
-  static constexpr int ATOMS = (D + 63) / 64;
-  static constexpr int Q_ATOM = kHalfRows * 128;   // 128 rows x 128 B
-  static constexpr int KV_ATOM = kKeyTile * 128;   // 128 keys x 128 B
-  static constexpr int Q_BYTES = ATOMS * Q_ATOM;   // Q of one half
-  static constexpr int KV_BYTES = ATOMS * KV_ATOM;             // one K or V range: a ring slot
-  // mbarriers (8 bytes each): per ring slot full, empty, raw (8-bit codes
-  // landed; bf16 caches: V range g % kMaxSlots put back to bf16) and conv
-  // (8-bit caches: both converter warps hold a slot's codes; bf16 caches: V
-  // range g % kMaxSlots rewritten); per half s
-  // (S complete), p (P written), o (P V complete), qf (Q stored), qe (the MMA
-  // warp has seen qf); per unit slot uf (record published), ue (record read);
-  // per (half, lane quadrant) the softmax pair's exchange; drain
-  static constexpr int B_FULL = 0, B_EMPTY = kMaxSlots, B_RAW = 2 * kMaxSlots, B_CONV = 3 * kMaxSlots;
-  static constexpr int B_S = 4 * kMaxSlots, B_P = B_S + kHalves, B_O = B_P + kHalves, B_QF = B_O + kHalves;
-  static constexpr int B_QE = B_QF + kHalves, B_UF = B_QE + kHalves, B_UE = B_UF + kUnitSlots;
-  static constexpr int B_X = B_UE + kUnitSlots, B_DRAIN = B_X + 4 * kHalves, B_SC = B_DRAIN + 1;
-  static constexpr int NBARS = B_SC + kScaleSlotsMax;  // sc: a range's block scales are in shared memory
-  static constexpr int XCH_BYTES = kHalves * kParts * kHalfRows * 4;  // one float per (half, part, row)
-  static constexpr int UNIT_BYTES = kUnitSlots * 32;                  // records of eight ints
-  static constexpr int VF_BYTES = kMaxSlots * 8;                      // per V range and converter warp: kept bf16
-  static constexpr int FIXED = kHalves * Q_BYTES + XCH_BYTES + UNIT_BYTES + VF_BYTES + 8 * NBARS + 16;
-  static constexpr int FIT = (227 * 1024 - FIXED) / KV_BYTES;
-  static constexpr int SLOTS = FIT < kMaxSlots ? FIT : kMaxSlots;
-  // Block scales of a range (scale_slot_bytes), SCALE_SLOTS of them in turn.
-  // The producer writes range g's once the ring slot of K(g) is free, that is,
-  // once load 2 g - SLOTS has been used up: V of range g - (SLOTS + 1) / 2 (odd
-  // SLOTS; its P is written) or K of range g - SLOTS / 2 (even; S of a range
-  // is issued only after both halves' P of the range before it). So the
-  // softmax warps have finished with range g - SCALE_SLOTS.
-  static constexpr int SCALE_SLOTS = SLOTS / 2 + 1;
-  static_assert(SCALE_SLOTS <= kScaleSlotsMax, "a barrier per scale slot");
-  static_assert(SLOTS >= 4, "the ring holds at least K and V of two ranges");
-  static constexpr int Q_OFF = 0;                                // Q of halves A and B
-  static constexpr int RING_OFF = Q_OFF + kHalves * Q_BYTES;     // K(0), V(0), K(1), V(1), ... in SLOTS slots
-  static constexpr int XCH_OFF = RING_OFF + SLOTS * KV_BYTES;    // the softmax pairs' exchange
-  static constexpr int UNIT_OFF = XCH_OFF + XCH_BYTES;           // unit records
-  static constexpr int VF_OFF = UNIT_OFF + UNIT_BYTES;           // V range flags (bf16 V rewritten as fp16)
-  static constexpr int BAR_OFF = VF_OFF + VF_BYTES;
-  static constexpr int TMEM_OFF = BAR_OFF + 8 * NBARS;
-  static constexpr int SC_OFF = TMEM_OFF + 16;
-  static constexpr int BYTES = SC_OFF + SCALE_SLOTS * kScaleSlotBytes;
-  // Shared memory requested per CTA: more than half an SM's, so that a second
-  // CTA (which would wait for TMEM) never lands on the same SM.
-  static constexpr int REQUEST = BYTES > 116 * 1024 ? BYTES : 116 * 1024;
-  // byte offset of 16-byte chunk c of row r in a swizzled tile with `atom` bytes per atom column
-  static __device__ __forceinline__ uint32_t off(int r, int c, int atom) {
-    return (c >> 3) * atom + r * 128 + (((c & 7) ^ (r & 7)) << 4);
-  }
-};
-static_assert(TcLayout<128>::BYTES <= 227 * 1024, "shared memory of one CTA");
-static_assert(TcLayout<128>::SLOTS >= 5, "loads run two ranges ahead at head_dim 128");
-
-// Bounded wait by a whole warp; the outcome is made warp-uniform, so a warp
-// that gives up leaves its loops together (no lane is left inside a
-// warp-collective instruction). A warp waits out at most one timeout.
-__device__ __forceinline__ void wait_warp(uint32_t bar, uint32_t parity, bool &failed) {
-  if (!failed) failed = !mbar_wait_bounded(bar, parity, kTcWaitTimeoutNs);
-  failed = __any_sync(0xffffffffu, failed);
-}
-
-// The two 32-bit words of a 128-byte-swizzle shared-memory descriptor (the
-// layout sw128_desc builds). The low word holds the start address >> 4 in
-// bits 0-13, so a tile's descriptors differ from its first one by adding the
-// byte offset >> 4 to the low word (shared addresses stay below 256 KB: no
-// carry out of the field). Building them once per unit keeps the issuing
-// thread at two additions per MMA: it shares its scheduler with two softmax
-// warps, and the tensor core queues only a couple of instructions.
-__device__ __forceinline__ uint32_t desc_lo(uint32_t smem_addr, uint32_t lbo) {
-  return ((smem_addr & 0x3FFFFu) >> 4) | (((lbo >> 4) & 0x3FFFu) << 16);
-}
-__host__ __device__ constexpr uint32_t desc_hi(uint32_t sbo) {
-  return ((sbo >> 4) & 0x3FFFu) | (1u << 14) | (2u << 29);  // SBO, version (bit 46), 128-byte swizzle (61-63)
-}
-// D[tmem] (+)= A[smem] * B[smem] with descriptors given as words; ACC = 0 overwrites D.
-template <int ACC>
-__device__ __forceinline__ void mma_ss(uint32_t d_tmem, uint32_t a_lo, uint32_t a_hi, uint32_t b_lo, uint32_t b_hi,
-                                       uint32_t idesc) {
-  asm volatile(
-      "{\n .reg .pred p;\n .reg .b64 a, b;\n setp.ne.b32 p, %6, 0;\n mov.b64 a, {%1, %2};\n"
-      " mov.b64 b, {%3, %4};\n tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %5, p;\n}\n" ::"r"(d_tmem),
-      "r"(a_lo), "r"(a_hi), "r"(b_lo), "r"(b_hi), "r"(idesc), "n"(ACC)
-      : "memory");
-}
-// D[tmem] (+)= A[tmem] * B[smem].
-template <int ACC>
-__device__ __forceinline__ void mma_ts(uint32_t d_tmem, uint32_t a_tmem, uint32_t b_lo, uint32_t b_hi, uint32_t idesc) {
-  asm volatile(
-      "{\n .reg .pred p;\n .reg .b64 b;\n setp.ne.b32 p, %5, 0;\n mov.b64 b, {%2, %3};\n"
-      " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], b, %4, p;\n}\n" ::"r"(d_tmem),
-      "r"(a_tmem), "r"(b_lo), "r"(b_hi), "r"(idesc), "n"(ACC)
-      : "memory");
-}
-
-// Block scales of 16 keys: (K factor, log2 V scale, 1 / V scale, -) of a
-// 16-key group, or (K factor, log2 V scale) of two 8-key groups.
-__device__ __forceinline__ float4 ld_scales(uint32_t addr) {
-  float4 v;
-  asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];\n"
-               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
-               : "r"(addr)
-               : "memory");
-  return v;
-}
-
-// 32 consecutive 32-bit columns of this thread's TMEM lane; the wait is in
-// the same statement, so no use of the registers can be scheduled before it.
-__device__ __forceinline__ void tmem_ld32_wait(uint32_t taddr, uint32_t (&r)[32]) {
-  asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];\n"
-      "tcgen05.wait::ld.sync.aligned;\n"
-      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
-      : "r"(taddr)
-      : "memory");
-}
-
-// The same for 16 columns.
-__device__ __forceinline__ void tmem_ld16_wait(uint32_t taddr, uint32_t (&r)[16]) {
-  asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];\n"
-      "tcgen05.wait::ld.sync.aligned;\n"
-      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
-      : "r"(taddr)
-      : "memory");
-}
-
-// Packed pairs of fp32 operations (one instruction for two lanes of data).
-__device__ __forceinline__ void fma2(float &d0, float &d1, float a0, float a1, float b0, float b1, float c0, float c1) {
-  asm("{\n .reg .b64 a, b, c, d;\n mov.b64 a, {%2, %3};\n mov.b64 b, {%4, %5};\n mov.b64 c, {%6, %7};\n"
-      " fma.rn.f32x2 d, a, b, c;\n mov.b64 {%0, %1}, d;\n}\n"
-      : "=f"(d0), "=f"(d1)
-      : "f"(a0), "f"(a1), "f"(b0), "f"(b1), "f"(c0), "f"(c1));
-}
-__device__ __forceinline__ void add2(float &d0, float &d1, float a0, float a1, float b0, float b1) {
-  asm("{\n .reg .b64 a, b, d;\n mov.b64 a, {%2, %3};\n mov.b64 b, {%4, %5};\n add.rn.f32x2 d, a, b;\n"
-      " mov.b64 {%0, %1}, d;\n}\n"
-      : "=f"(d0), "=f"(d1)
-      : "f"(a0), "f"(a1), "f"(b0), "f"(b1));
-}
-__device__ __forceinline__ void sub2(float &d0, float &d1, float a0, float a1, float b0, float b1) {
-  asm("{\n .reg .b64 a, b, d;\n mov.b64 a, {%2, %3};\n mov.b64 b, {%4, %5};\n sub.rn.f32x2 d, a, b;\n"
-      " mov.b64 {%0, %1}, d;\n}\n"
-      : "=f"(d0), "=f"(d1)
-      : "f"(a0), "f"(a1), "f"(b0), "f"(b1));
-}
-__device__ __forceinline__ float max3(float a, float b, float c) {
-  float d;
-  asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
-  return d;
-}
-
-// Row maximum of 32 raw scores, key ck0 + i visible while ck0 + i < lim.
-__device__ __forceinline__ float masked_max32(const uint32_t (&s)[32], int ck0, int lim) {
-  float m = -INFINITY;
-  if (ck0 + 32 <= lim) {
-    // a tree of depth 4 (a chain of 16 three-input maxima would be 16 deep)
-    float t[8];
-#pragma unroll
-    for (int i = 0; i < 8; ++i)
-      t[i] = max3(__uint_as_float(s[4 * i]), __uint_as_float(s[4 * i + 1]),
-                  fmaxf(__uint_as_float(s[4 * i + 2]), __uint_as_float(s[4 * i + 3])));
-    m = max3(max3(t[0], t[1], t[2]), max3(t[3], t[4], t[5]), fmaxf(t[6], t[7]));
-  } else {
-#pragma unroll
-    for (int i = 0; i < 32; ++i) m = ck0 + i < lim ? fmaxf(m, __uint_as_float(s[i])) : m;
-  }
-  return m;
-}
-
-// Row maximum of 32 scores under block scales (at shared address sc): s * (rowf * kf) + lv per group, as separately rounded operations. kf
-// and rowf are positive, so a group's largest raw score gives its largest
-// scaled one.
-template <int GRP>
-__device__ __forceinline__ float scaled_max32(const uint32_t (&s)[32], int ck0, int lim, float rowf, uint32_t sc) {
-  float m = -INFINITY;
-  float4 v;
-#pragma unroll
-  for (int g = 0; g < 32 / GRP; ++g) {
-    constexpr int PER16 = 16 / GRP;  // groups per 16 keys
-    if (g % PER16 == 0) v = ld_scales(sc + 16 * (g / PER16));
-    const float kf = g % PER16 == 0 ? v.x : v.z, lv = g % PER16 == 0 ? v.y : v.w;
-    float t;
-    if (ck0 + 32 <= lim) {
-      t = max3(__uint_as_float(s[GRP * g]), __uint_as_float(s[GRP * g + 1]), __uint_as_float(s[GRP * g + 2]));
-      float u = max3(__uint_as_float(s[GRP * g + 3]), __uint_as_float(s[GRP * g + 4]), __uint_as_float(s[GRP * g + 5]));
-#pragma unroll
-      for (int i = 6; i < GRP; i += 4) {
-        t = max3(t, __uint_as_float(s[GRP * g + i]), __uint_as_float(s[GRP * g + i + 1]));
-        if (i + 3 < GRP) u = max3(u, __uint_as_float(s[GRP * g + i + 2]), __uint_as_float(s[GRP * g + i + 3]));
-      }
-      t = fmaxf(t, u);
-    } else {
-      t = -INFINITY;
-#pragma unroll
-      for (int i = 0; i < GRP; ++i) t = ck0 + GRP * g + i < lim ? fmaxf(t, __uint_as_float(s[GRP * g + i])) : t;
-    }
-    m = fmaxf(m, __fadd_rn(__fmul_rn(t, __fmul_rn(rowf, kf)), lv));
-  }
-  return m;
-}
-
-// Store 8 32-bit columns (raw bits) of this thread's TMEM lane.
-__device__ __forceinline__ void tmem_st8u(uint32_t taddr, const uint32_t (&v)[8]) {
-  asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};\n" ::"r"(taddr), "r"(v[0]),
-      "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
-      : "memory");
-}
 
 // P for the 16 keys of one UMMA K step (scores s[0..16), key k0 + i visible
 // while k0 + i < lim): p = 2^(s * sl2 - ms), summed into *sum and stored at
@@ -368,44 +114,6 @@ __device__ __forceinline__ void probs16_store(const uint32_t *s, int k0, int lim
   if (SPLIT) tmem_st8u(col + 8, lv);
 }
 
-// The same for 16 keys under block scales `c`, one fp16 P per key:
-// P' = 2^(s * kf + lv - ms) carries the V scale 2^lv, so O accumulates P' times
-// codes; the row sum takes P' / 2^lv. EXACT rows also apply the row's factor
-// (1 otherwise).
-template <int GRP, bool EXACT>
-__device__ __forceinline__ void probs16_scaled_store(const uint32_t *s, int k0, int lim, float rowf, float ms,
-                                                     float &sum, uint32_t col, const float4 &c) {
-  const bool full = k0 + 16 <= lim;
-  uint32_t hv[8];
-#pragma unroll
-  for (int g = 0; g < 16 / GRP; ++g) {
-    const float kf = g == 0 ? c.x : c.z, lv = g == 0 ? c.y : c.w;
-    const float f = EXACT ? __fmul_rn(rowf, kf) : kf, add = lv - ms;
-    float acc0 = 0.f, acc1 = 0.f;
-#pragma unroll
-    for (int j = 0; j < GRP / 2; ++j) {
-      const int i = GRP / 2 * g + j;
-      float x0 = __uint_as_float(s[2 * i]), x1 = __uint_as_float(s[2 * i + 1]);
-      if (!full) {
-        x0 = k0 + 2 * i < lim ? x0 : -INFINITY;
-        x1 = k0 + 2 * i + 1 < lim ? x1 : -INFINITY;
-      }
-      float e0, e1;
-      if (EXACT) {
-        e0 = __fsub_rn(__fadd_rn(__fmul_rn(x0, f), lv), ms);
-        e1 = __fsub_rn(__fadd_rn(__fmul_rn(x1, f), lv), ms);
-      } else {
-        fma2(e0, e1, x0, x1, f, f, add, add);
-      }
-      const float p0 = ex2_approx(e0), p1 = ex2_approx(e1);
-      add2(acc0, acc1, acc0, acc1, p0, p1);
-      hv[i] = ElemFp16::pack(p0, p1);
-    }
-    sum = fmaf(acc0 + acc1, GRP == 16 ? c.z : ex2_approx(-lv), sum);
-  }
-  tmem_st8u(col, hv);
-}
-
 // P of one softmax warp's 64 keys of a range, from column sp of its lane,
 // the scores read again from TMEM 32 at a time (P of the first 32 keys never
 // covers the columns of the second). PAIR: a bf16 hi + lo pair per key, 16
@@ -436,57 +144,10 @@ __device__ __forceinline__ void range_probs(uint32_t sp, int ck0, int lim, float
   }
 }
 
-// Two 32-column loads of this thread's TMEM lane, then one wait.
-__device__ __forceinline__ void tmem_ld32x2_wait(uint32_t taddr, uint32_t (&a)[32], uint32_t (&b)[32]) {
-  asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];\n"
-      : "=r"(a[0]), "=r"(a[1]), "=r"(a[2]), "=r"(a[3]), "=r"(a[4]), "=r"(a[5]), "=r"(a[6]), "=r"(a[7]), "=r"(a[8]), "=r"(a[9]), "=r"(a[10]), "=r"(a[11]), "=r"(a[12]), "=r"(a[13]), "=r"(a[14]), "=r"(a[15]), "=r"(a[16]), "=r"(a[17]), "=r"(a[18]), "=r"(a[19]), "=r"(a[20]), "=r"(a[21]), "=r"(a[22]), "=r"(a[23]), "=r"(a[24]), "=r"(a[25]), "=r"(a[26]), "=r"(a[27]), "=r"(a[28]), "=r"(a[29]), "=r"(a[30]), "=r"(a[31])
-      : "r"(taddr)
-      : "memory");
-  asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];\n"
-      "tcgen05.wait::ld.sync.aligned;\n"
-      : "=r"(b[0]), "=r"(b[1]), "=r"(b[2]), "=r"(b[3]), "=r"(b[4]), "=r"(b[5]), "=r"(b[6]), "=r"(b[7]), "=r"(b[8]), "=r"(b[9]), "=r"(b[10]), "=r"(b[11]), "=r"(b[12]), "=r"(b[13]), "=r"(b[14]), "=r"(b[15]), "=r"(b[16]), "=r"(b[17]), "=r"(b[18]), "=r"(b[19]), "=r"(b[20]), "=r"(b[21]), "=r"(b[22]), "=r"(b[23]), "=r"(b[24]), "=r"(b[25]), "=r"(b[26]), "=r"(b[27]), "=r"(b[28]), "=r"(b[29]), "=r"(b[30]), "=r"(b[31])
-      : "r"(taddr + 32)
-      : "memory");
-}
-
-// Block scales of the group that starts at `key` (this KV head); left as
-// they are past the last key or for a block id out of range. p.k_scales and
-// p.v_scales may have been written shortly before: not an invariant load.
-__device__ __forceinline__ void block_scales_of(const TileParams &p, const int32_t *table, int key, int kv_end, int kvh,
-                                                float &ks, float &vs) {
-  if (key >= kv_end) return;
-  const int phys = __ldg(table + (key >> p.block_shift));
-  if (phys < 0 || phys >= p.num_blocks) return;
-  const int64_t at = static_cast<int64_t>(phys) * p.num_kv_heads + kvh;
-  ks = ld_cg(p.k_scales + at);
-  vs = ld_cg(p.v_scales + at);
-}
-template <int GRP>
-__device__ __forceinline__ void st_scales(uint32_t slot, int group, float kf, float vs) {
-  const float lv = __log2f(vs);
-  if (GRP == 16)
-    asm volatile("st.shared.v4.f32 [%0], {%1, %2, %3, %3};\n" ::"r"(slot + 16 * group), "f"(kf), "f"(lv),
-                 "f"(__fdividef(1.f, vs))
-                 : "memory");
-  else
-    asm volatile("st.shared.v2.f32 [%0], {%1, %2};\n" ::"r"(slot + 8 * group), "f"(kf), "f"(lv) : "memory");
-}
-
 // A published unit: a tile of one request and one KV head, or the end of the stream.
-// With block scales a unit may be a part of a tile's keys (kv_begin a multiple
-// of 128) whose rows go to partial slot `slot` (-1: the output).
 struct TileUnit {
-  int b, row0, npos, pos0, kv_end, kvh, stop, kv_begin, slot;
+  int b, row0, npos, pos0, kv_end, kvh, stop;
 };
-
-// The key range of a unit with block scales: a whole tile's keys, or a part of
-// them with a partial slot that exists.
-__device__ __forceinline__ bool part_sane(const TileUnit &r, const TileParams &p, int item) {
-  if (r.kv_begin < 0 || r.kv_begin % kKeyTile != 0 || r.kv_begin >= r.kv_end || r.kv_end > r.pos0 + r.npos) return false;
-  return r.slot < 0 ? r.kv_begin == 0 && r.kv_end == r.pos0 + r.npos : item < p.max_part_items;
-}
 
 // A bf16 V range in shared memory, rewritten by the two converter warps:
 // converter warp w takes its 16-byte chunks c = w * PER * 32 + lane + 32 i
@@ -573,11 +234,7 @@ __device__ __forceinline__ void vrange_back_to_bf16(uint32_t sV, int c0, int nva
 // bf16 and its flags send the softmax warps and the MMA warp to the hi + lo
 // pair for that range. Either way the rows past the unit's last key are
 // zeroed.
-//
-// With block scales (BSC, the keys of a group) the producer also stages each
-// range's scales, which the softmax warps fold into the exponents as the decode
-// kernel does (probs16_scaled_store).
-template <int D, int G, typename E, bool KV8, int BSC>
+template <int D, int G, typename E, bool KV8>
 // Twenty warps (two of them idle over fp16 caches), one CTA per SM.
 __global__ void __launch_bounds__(KV8 ? kTileThreads8 : kTileThreads, 1)
     prefill_tile_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap,
@@ -650,7 +307,6 @@ __global__ void __launch_bounds__(KV8 ? kTileThreads8 : kTileThreads, 1)
       mbar_init(bar(Lay::B_UE + i), 1 + kSoftmaxWarps + (KV8 || VCONV ? kConvWarps : 0));
     }
     for (int i = 0; i < 4 * kHalves; ++i) mbar_init(bar(Lay::B_X + i), 32 * kParts);
-    for (int i = 0; i < kScaleSlotsMax; ++i) mbar_init(bar(Lay::B_SC + i), 1);
     mbar_init(bar(Lay::B_DRAIN), 1);
     prefetch_tmap(&kmap);
     prefetch_tmap(&vmap);
@@ -680,14 +336,13 @@ __global__ void __launch_bounds__(KV8 ? kTileThreads8 : kTileThreads, 1)
     r.stop = 1;
     if (!failed) {
       const volatile int *u = units + 8 * s;
-      r.slot = u[0];
+      r.b = u[0];
       r.row0 = u[1];
       r.npos = u[2];
       r.pos0 = u[3];
       r.kv_end = u[4];
       r.kvh = u[5];
       r.stop = u[6];
-      r.kv_begin = BSC ? u[7] : 0;
     }
     __syncwarp();
     if (lane == 0 && !failed) mbar_arrive(bar(Lay::B_UE + s));
@@ -697,14 +352,9 @@ __global__ void __launch_bounds__(KV8 ? kTileThreads8 : kTileThreads, 1)
 #pragma unroll
     for (int h = 0; h < kHalves; ++h) {
       const int last = min(r.npos, (h + 1) * POS_PER_HALF);  // positions [h * POS_PER_HALF, last)
-      if constexpr (BSC)  // of this part
-        nh[h] = last > h * POS_PER_HALF
-                    ? max((min(r.pos0 + last, r.kv_end) - r.kv_begin + kKeyTile - 1) / kKeyTile, 0)
-                    : 0;
-      else
-        nh[h] = last > h * POS_PER_HALF ? (r.pos0 + last + kKeyTile - 1) / kKeyTile : 0;
+      nh[h] = last > h * POS_PER_HALF ? (r.pos0 + last + kKeyTile - 1) / kKeyTile : 0;
     }
-    return (r.kv_end - (BSC ? r.kv_begin : 0) + kKeyTile - 1) / kKeyTile;
+    return (r.kv_end + kKeyTile - 1) / kKeyTile;
   };
   // V in shared memory. VBLK: block after block of R = block_size rows, each
   // [atom][R rows][128 B]; else [atom][128 keys][128 B] (per-atom boxes).
@@ -730,7 +380,7 @@ __global__ void __launch_bounds__(KV8 ? kTileThreads8 : kTileThreads, 1)
       int u = 0;
       if (lane == 0) u = atomicAdd(p.tile_counter, 1);
       u = __shfl_sync(FULL, u, 0);
-      TileUnit r{0, 0, 0, 0, 0, 0, u >= total_units ? 1 : 0, 0, -1};
+      TileUnit r{0, 0, 0, 0, 0, 0, u >= total_units ? 1 : 0};
       if (!r.stop) {
         const int item = u / Hkv;
         r.kvh = u - item * Hkv;
@@ -741,13 +391,9 @@ __global__ void __launch_bounds__(KV8 ? kTileThreads8 : kTileThreads, 1)
         r.npos = r0.z;
         r.pos0 = r0.w;
         r.kv_end = r1.y;
-        if constexpr (BSC != 0) {
-          r.kv_begin = r1.x;
-          r.slot = r1.z >= 0 ? item * Hkv + r.kvh : -1;
-        }
         const bool sane = r.b >= 0 && r.b < p.num_seqs && r.npos >= 1 && r.npos <= kPrefillTileRows / G &&
                           r.row0 >= 0 && r.row0 + r.npos <= p.total_q && r.pos0 >= 0 &&
-                          (BSC ? part_sane(r, p, item) : r.kv_end == r.pos0 + r.npos) &&
+                          r.kv_end == r.pos0 + r.npos &&
                           r.kv_end <= static_cast<int64_t>(p.max_blocks_per_seq) * bs;
         if (!sane) {
           if (lane == 0) flag_error(p.status, PA_FLAG_LENGTHS);
@@ -759,14 +405,13 @@ __global__ void __launch_bounds__(KV8 ? kTileThreads8 : kTileThreads, 1)
       if (failed) break;
       if (lane == 0) {
         volatile int *d = units + 8 * s;
-        d[0] = BSC ? r.slot : -1;
+        d[0] = r.b;
         d[1] = r.row0;
         d[2] = r.npos;
         d[3] = r.pos0;
         d[4] = r.kv_end;
         d[5] = r.kvh;
         d[6] = r.stop;
-        if (BSC) d[7] = r.kv_begin;
         mbar_arrive(bar(Lay::B_UF + s));  // release: the record is visible to whoever sees the phase
       }
       __syncwarp();
@@ -790,26 +435,12 @@ __global__ void __launch_bounds__(KV8 ? kTileThreads8 : kTileThreads, 1)
       for (int kt = 0; kt < nkt && !failed; ++kt) {
         // lane i computes the row coordinate of K box i and V box i of this
         // range, and issues those boxes itself once lane 0 has set the byte count
-        const int key0 = (BSC ? r.kv_begin : 0) + kt * kKeyTile;  // first key of the range
-        const int zk = lane < nbk ? box_z(key0 + lane * box_rows, box_rows) : 0;
-        const int zv = VBLK ? (lane < nbv ? box_z(key0 + lane * bs, bs) : 0) : zk;
-        float gks = 1.f, gvs1 = 1.f;  // block scales of group `lane` (1 past the last key)
-        if constexpr (BSC != 0) {
-          if (lane < kKeyTile / BSC) block_scales_of(p, table, key0 + BSC * lane, r.kv_end, r.kvh, gks, gvs1);
-        }
+        const int zk = lane < nbk ? box_z(kt * kKeyTile + lane * box_rows, box_rows) : 0;
+        const int zv = VBLK ? (lane < nbv ? box_z(kt * kKeyTile + lane * bs, bs) : 0) : zk;
         for (int v = 0; v < 2 && !failed; ++v) {
           const uint32_t slot = g % SLOTS, use = g / SLOTS;
           if (use > 0) wait_warp(bar(Lay::B_EMPTY + slot), (use - 1) & 1u, failed);
           if (failed) break;
-          if constexpr (BSC != 0) {
-            if (v == 0) {
-              const uint32_t fi = (g / 2) % Lay::SCALE_SLOTS;
-              if (lane < kKeyTile / BSC)
-                st_scales<BSC>(base + Lay::SC_OFF + fi * kScaleSlotBytes, lane, gks * p.scale_log2, gvs1);
-              __syncwarp();
-              if (lane == 0) mbar_arrive(bar(Lay::B_SC + fi));  // release: the range's scales
-            }
-          }
           const void *map = v ? static_cast<const void *>(&vmap) : static_cast<const void *>(&kmap);
           const uint32_t dst = sRing + slot * Lay::KV_BYTES;
           if constexpr (KV8) {
@@ -1045,7 +676,7 @@ __global__ void __launch_bounds__(KV8 ? kTileThreads8 : kTileThreads, 1)
           } else if (h == first_reader(kt)) {
             wait_warp(bar(Lay::B_FULL + vslot), full_parity(kt, 1), failed);
             if (failed) break;
-            const int key0 = (BSC ? r.kv_begin : 0) + kt * kKeyTile;
+            const int key0 = kt * kKeyTile;
             if (key0 + kKeyTile > r.kv_end) {
               // rows of keys past kv_end may hold anything (even NaN): zero them in V
               const uint32_t sV = sRing + vslot * Lay::KV_BYTES;
@@ -1156,7 +787,7 @@ __global__ void __launch_bounds__(KV8 ? kTileThreads8 : kTileThreads, 1)
         }
         return w;
       };
-      float sl2 = BSC ? 1.f : p.scale_log2;  // > 0: the max of raw scores gives the max of scaled ones
+      float sl2 = p.scale_log2;  // > 0: the max of raw scores gives the max of scaled ones
       float qmul = 1.f;
       if constexpr (KV8 && std::is_same<E, ElemBf16>::value) {
         // bf16 rows over 8-bit caches: 2^-e, e > 0 only when the row's largest |q| reaches 2^15
@@ -1207,18 +838,10 @@ __global__ void __launch_bounds__(KV8 ? kTileThreads8 : kTileThreads, 1)
       const int lim = row_valid ? cur.pos0 + qi + 1 : 0;  // keys j < lim are visible to this row
       float m_used = -INFINITY, l = 0.f;
       for (int kt = 0; kt < nk; ++kt) {
-        const int ck0 = (BSC ? cur.kv_begin : 0) + kt * kKeyTile + part * PART_KEYS;  // this warp's first key of the range
+        const int ck0 = kt * kKeyTile + part * PART_KEYS;  // this warp's first key of the range
         const uint32_t sp = t_lane + Tm::SP + part * PART_KEYS;
         wait_warp(bar(Lay::B_S + h), (phh + kt) & 1u, failed);
         if (failed) break;
-        uint32_t sc = 0;  // block scales: this warp's keys of the range
-        if constexpr (BSC != 0) {
-          // (already there: they were written before the K that S came from)
-          const uint32_t gv = gvs + kt, fi = gv % Lay::SCALE_SLOTS;
-          wait_warp(bar(Lay::B_SC + fi), (gv / Lay::SCALE_SLOTS) & 1u, failed);
-          if (failed) break;
-          sc = base + Lay::SC_OFF + fi * kScaleSlotBytes + part * (kScaleSlotBytes / kParts);
-        }
         tc_fence_after();
         uint32_t s0[32], s1[32];
         tmem_ld32x2_wait(sp, s0, s1);
@@ -1226,16 +849,10 @@ __global__ void __launch_bounds__(KV8 ? kTileThreads8 : kTileThreads, 1)
         // m_used, as separately rounded operations (no contraction into one
         // fused multiply-add): the exponents below are bounded by exactly this
         // difference. The other warp reads its scores before either writes P.
-        float mx;
-        if constexpr (BSC != 0) {
-          mx = scaled_max32<BSC>(s0, ck0, lim, sl2, sc);
-          mx = fmaxf(mx, scaled_max32<BSC>(s1, ck0 + 32, lim, sl2, sc + 32));
-        } else {
-          mx = fmaxf(masked_max32(s0, ck0, lim), masked_max32(s1, ck0 + 32, lim));
-        }
+        const float mx = fmaxf(masked_max32(s0, ck0, lim), masked_max32(s1, ck0 + 32, lim));
         const float mo = exchange(mx);
         if (failed) break;
-        const float cm = BSC ? fmaxf(mx, mo) : __fmul_rn(sl2, fmaxf(mx, mo));
+        const float cm = __fmul_rn(sl2, fmaxf(mx, mo));
         const bool grow = cm > -INFINITY && (m_used == -INFINITY || __fsub_rn(cm, m_used) > kRescaleLog2);
         float alpha = 1.f;  // factor owed by O and l for the growth
         if (grow) {
@@ -1244,8 +861,7 @@ __global__ void __launch_bounds__(KV8 ? kTileThreads8 : kTileThreads, 1)
         }
         const float ms = m_used == -INFINITY ? 0.f : m_used;
         float sum = 0.f;
-        // (block scales: sl2 is the row's factor, 1 unless its q was scaled)
-        const bool exact = __any_sync(FULL, fabsf(ms) > 4096.f || (BSC != 0 && sl2 != 1.f));
+        const bool exact = __any_sync(FULL, fabsf(ms) > 4096.f);
         bool vpair = false;  // V(kt) kept bf16 (bf16 caches only): P as a hi + lo pair
         if constexpr (VCONV) {
           const uint32_t gv = gvs + kt, fi = gv % kMaxSlots;
@@ -1261,25 +877,7 @@ __global__ void __launch_bounds__(KV8 ? kTileThreads8 : kTileThreads, 1)
         // P of step ks (8 columns at 8 ks) covers only scores read by
         // earlier steps. Rare cases stay out of the loop (inside it, as a
         // branch per step, they cost 2 %).
-        if constexpr (BSC != 0) {
-          if (exact) {
-#pragma unroll 1
-            for (int ks = 0; ks < PART_KEYS / 16; ++ks) {
-              const float4 c = ld_scales(sc + 16 * ks);
-              uint32_t t[16];
-              tmem_ld16_wait(sp + 16 * ks, t);
-              probs16_scaled_store<BSC, true>(t, ck0 + 16 * ks, lim, sl2, ms, sum, sp + 8 * ks, c);
-            }
-          } else {
-#pragma unroll 2
-            for (int ks = 0; ks < PART_KEYS / 16; ++ks) {
-              const float4 c = ld_scales(sc + 16 * ks);
-              uint32_t t[16];
-              tmem_ld16_wait(sp + 16 * ks, t);
-              probs16_scaled_store<BSC, false>(t, ck0 + 16 * ks, lim, sl2, ms, sum, sp + 8 * ks, c);
-            }
-          }
-        } else if (vpair) {
+        if (vpair) {
           range_probs<true>(sp, ck0, lim, sl2, ms, exact, sum);
         } else if (exact) {
           range_probs<false>(sp, ck0, lim, sl2, ms, true, sum);
@@ -1332,29 +930,11 @@ __global__ void __launch_bounds__(KV8 ? kTileThreads8 : kTileThreads, 1)
         const float inv = lt > 0.f ? p.out_scale / lt : 0.f;
         bf16 *dst = p.out + static_cast<int64_t>(cur.row0 + (row_valid ? qi : 0)) * p.num_heads * D +
                     static_cast<int64_t>(cur.kvh * G + g) * D;
-        float *pdst = nullptr;  // the row's partial, for a part of the tile's keys
-        if constexpr (BSC != 0) {
-          if (cur.slot >= 0) {
-            const int64_t prow = static_cast<int64_t>(cur.slot) * kPrefillTileRows + h * kHalfRows + r;
-            pdst = p.part_o + prow * D;
-            if (part == 0 && row_valid) p.part_lse[prow] = lt != 0.f ? m_used + __log2f(lt) : -INFINITY;
-          }
-        }
 #pragma unroll 1
         for (int ch = ch0; ch < ch1; ++ch) {
           uint32_t t[32];
           tmem_ld32_wait(t_lane + Tm::O + ch * 32, t);
-          if (BSC && pdst) {
-            if (row_valid) {
-#pragma unroll
-              for (int c = 0; c < 8; ++c) {
-                if (32 * ch + 4 * c >= D) continue;
-                const float *f = reinterpret_cast<const float *>(&t[4 * c]);
-                *reinterpret_cast<float4 *>(pdst + ch * 32 + 4 * c) =
-                    make_float4(f[0] * inv, f[1] * inv, f[2] * inv, f[3] * inv);
-              }
-            }
-          } else if (row_valid) {
+          if (row_valid) {
 #pragma unroll
             for (int c = 0; c < 4; ++c) {
               if (32 * ch + 8 * c >= D) continue;  // head_dim 80: the last 16 columns are padding
@@ -1366,9 +946,6 @@ __global__ void __launch_bounds__(KV8 ? kTileThreads8 : kTileThreads, 1)
           }
         }
         tc_fence_before();  // O is overwritten by a later unit's first product
-      } else if (BSC && cur.slot >= 0 && part == 0 && row_valid) {
-        // the half sees none of this part's keys
-        p.part_lse[static_cast<int64_t>(cur.slot) * kPrefillTileRows + h * kHalfRows + r] = -INFINITY;
       }
       phh += nk;
       gvs += nkt_all;
@@ -1433,10 +1010,7 @@ struct WideLayout {
   static constexpr int B_FULL = 0, B_EMPTY = kMaxSlots, B_RAW = 2 * kMaxSlots, B_CONV = 3 * kMaxSlots;
   static constexpr int B_S = 4 * kMaxSlots, B_P = B_S + 2, B_O = B_P + 2, B_QF = B_O + 1, B_QE = B_QF + 1;
   static constexpr int B_UF = B_QE + 1, B_UE = B_UF + kUnitSlots, B_X1 = B_UE + kUnitSlots, B_X2 = B_X1 + 4;
-  static constexpr int B_DRAIN = B_X2 + 4, B_SC = B_DRAIN + 1;
-  // Block scales: range g's are written once load 4 g - 5 (V of range g - 2) has been used up.
-  static constexpr int SCALE_SLOTS = 2;
-  static constexpr int NBARS = B_SC + SCALE_SLOTS;
+  static constexpr int B_DRAIN = B_X2 + 4, NBARS = B_DRAIN + 1;
   static constexpr int XCH_BYTES = kWideSoftmaxWarps * 32 * 4;
   static constexpr int REC_BYTES = kUnitSlots * 32;
   static constexpr int FIXED = Q_BYTES + XCH_BYTES + REC_BYTES + 8 * NBARS + 16;
@@ -1448,13 +1022,11 @@ struct WideLayout {
   static constexpr int REC_OFF = XCH_OFF + XCH_BYTES;
   static constexpr int BAR_OFF = REC_OFF + REC_BYTES;
   static constexpr int TMEM_OFF = BAR_OFF + 8 * NBARS;
-  static constexpr int SC_OFF = TMEM_OFF + 16;
-  static constexpr int BYTES = SC_OFF + SCALE_SLOTS * kScaleSlotBytes;
+  static constexpr int BYTES = TMEM_OFF + 16;
 };
-static_assert(WideLayout::SLOTS == 5, "two scale slots");
 static_assert(WideLayout::BYTES <= 227 * 1024, "shared memory of one CTA");
 
-template <int G, typename E, bool KV8, int BSC>
+template <int G, typename E, bool KV8>
 __global__ void __launch_bounds__(kWideThreads, 1)
     prefill_tile_wide_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap,
                              const TileParams p) {
@@ -1517,7 +1089,6 @@ __global__ void __launch_bounds__(kWideThreads, 1)
       mbar_init(bar(Lay::B_X1 + q), 64);  // the two softmax warps of a lane quadrant
       mbar_init(bar(Lay::B_X2 + q), 64);
     }
-    for (int i = 0; i < Lay::SCALE_SLOTS; ++i) mbar_init(bar(Lay::B_SC + i), 1);
     mbar_init(bar(Lay::B_DRAIN), 1);
     prefetch_tmap(&kmap);
     prefetch_tmap(&vmap);
@@ -1544,19 +1115,18 @@ __global__ void __launch_bounds__(kWideThreads, 1)
     r.stop = 1;
     if (!failed) {
       const volatile int *u = units + 8 * s;
-      r.slot = u[0];
+      r.b = u[0];
       r.row0 = u[1];
       r.npos = u[2];
       r.pos0 = u[3];
       r.kv_end = u[4];
       r.kvh = u[5];
       r.stop = u[6];
-      r.kv_begin = BSC ? u[7] : 0;
     }
     __syncwarp();
     if (lane == 0 && !failed) mbar_arrive(bar(Lay::B_UE + s));
   };
-  auto nranges = [&](const TileUnit &r) { return (r.kv_end - (BSC ? r.kv_begin : 0) + kKeyTile - 1) / kKeyTile; };
+  auto nranges = [&](const TileUnit &r) { return (r.kv_end + kKeyTile - 1) / kKeyTile; };
 
   if (warp == kTmaWarp) {
     // ---------------- producer ----------------
@@ -1569,7 +1139,7 @@ __global__ void __launch_bounds__(kWideThreads, 1)
       int u = 0;
       if (lane == 0) u = atomicAdd(p.tile_counter, 1);
       u = __shfl_sync(FULL, u, 0);
-      TileUnit r{0, 0, 0, 0, 0, 0, u >= total_units ? 1 : 0, 0, -1};
+      TileUnit r{0, 0, 0, 0, 0, 0, u >= total_units ? 1 : 0};
       if (!r.stop) {
         const int item = u / Hkv;
         r.kvh = u - item * Hkv;
@@ -1580,13 +1150,8 @@ __global__ void __launch_bounds__(kWideThreads, 1)
         r.npos = r0.z;
         r.pos0 = r0.w;
         r.kv_end = r1.y;
-        if constexpr (BSC != 0) {
-          r.kv_begin = r1.x;
-          r.slot = r1.z >= 0 ? item * Hkv + r.kvh : -1;
-        }
         const bool sane = r.b >= 0 && r.b < p.num_seqs && r.npos >= 1 && r.npos <= POS && r.row0 >= 0 &&
-                          r.row0 + r.npos <= p.total_q && r.pos0 >= 0 &&
-                          (BSC ? part_sane(r, p, item) : r.kv_end == r.pos0 + r.npos) &&
+                          r.row0 + r.npos <= p.total_q && r.pos0 >= 0 && r.kv_end == r.pos0 + r.npos &&
                           r.kv_end <= static_cast<int64_t>(p.max_blocks_per_seq) * bs;
         if (!sane) {
           if (lane == 0) flag_error(p.status, PA_FLAG_LENGTHS);
@@ -1598,14 +1163,13 @@ __global__ void __launch_bounds__(kWideThreads, 1)
       if (failed) break;
       if (lane == 0) {
         volatile int *d = units + 8 * s;
-        d[0] = BSC ? r.slot : -1;
+        d[0] = r.b;
         d[1] = r.row0;
         d[2] = r.npos;
         d[3] = r.pos0;
         d[4] = r.kv_end;
         d[5] = r.kvh;
         d[6] = r.stop;
-        if (BSC) d[7] = r.kv_begin;
         mbar_arrive(bar(Lay::B_UF + s));
       }
       __syncwarp();
@@ -1623,25 +1187,11 @@ __global__ void __launch_bounds__(kWideThreads, 1)
       };
       const int nkt = nranges(r);
       for (int kt = 0; kt < nkt && !failed; ++kt) {
-        const int key0 = (BSC ? r.kv_begin : 0) + kt * kKeyTile;  // first key of the range
-        const int z = lane < nbk ? box_z(key0 + lane * box_rows, box_rows) : 0;
-        float gks = 1.f, gvs1 = 1.f;  // block scales of group `lane` (1 past the last key)
-        if constexpr (BSC != 0) {
-          if (lane < kKeyTile / BSC) block_scales_of(p, table, key0 + BSC * lane, r.kv_end, r.kvh, gks, gvs1);
-        }
+        const int z = lane < nbk ? box_z(kt * kKeyTile + lane * box_rows, box_rows) : 0;
         for (int v = 0; v < LPR && !failed; ++v) {
           const uint32_t slot = g % SLOTS, use = g / SLOTS;
           if (use > 0) wait_warp(bar(Lay::B_EMPTY + slot), (use - 1) & 1u, failed);
           if (failed) break;
-          if constexpr (BSC != 0) {
-            if (v == 0) {
-              const uint32_t fi = (g / LPR) % Lay::SCALE_SLOTS;
-              if (lane < kKeyTile / BSC)
-                st_scales<BSC>(base + Lay::SC_OFF + fi * kScaleSlotBytes, lane, gks * p.scale_log2, gvs1);
-              __syncwarp();
-              if (lane == 0) mbar_arrive(bar(Lay::B_SC + fi));  // release: the range's scales
-            }
-          }
           const void *map = v >= 2 ? static_cast<const void *>(&vmap) : static_cast<const void *>(&kmap);
           const int x0 = (v & 1) * 128;  // first element of the unit's half of d
           const uint32_t dst = sRing + slot * Lay::UNIT_BYTES;
@@ -1780,7 +1330,7 @@ __global__ void __launch_bounds__(kWideThreads, 1)
         wait_warp(bar(Lay::B_FULL + vs0), full_parity(kt, 2), failed);
         wait_warp(bar(Lay::B_FULL + vs1), full_parity(kt, 3), failed);
         if (failed) break;
-        const int key0 = (BSC ? r.kv_begin : 0) + kt * kKeyTile;
+        const int key0 = kt * kKeyTile;
         if (key0 + kKeyTile > r.kv_end) {
           // rows of keys past kv_end may hold anything (even NaN): zero them in both V units
           const int vr0 = r.kv_end - key0;
@@ -1870,7 +1420,7 @@ __global__ void __launch_bounds__(kWideThreads, 1)
         }
         return w;
       };
-      float sl2 = BSC ? 1.f : p.scale_log2;
+      float sl2 = p.scale_log2;
       float qmul = 1.f;
       if constexpr (KV8 && std::is_same<E, ElemBf16>::value) {
         float amax = 0.f;
@@ -1919,28 +1469,17 @@ __global__ void __launch_bounds__(kWideThreads, 1)
       float m_used = -INFINITY, l = 0.f;
       for (int kt = 0; kt < nk; ++kt) {
         const uint32_t gr = ph + kt;
-        const int ck0 = (BSC ? cur.kv_begin : 0) + kt * kKeyTile + part * 64;
+        const int ck0 = kt * kKeyTile + part * 64;
         const uint32_t sp = tmem + lane_off + Tm::SP0 + (gr & 1u) * kKeyTile + part * 64;
         wait_warp(bar(Lay::B_S + (gr & 1u)), (gr >> 1) & 1u, failed);
         if (failed) break;
         tc_fence_after();
         uint32_t s0[32], s1[32];
         tmem_ld32x2_wait(sp, s0, s1);
-        uint32_t sc = 0;  // block scales: this warp's keys of the range
-        float mx;
-        if constexpr (BSC != 0) {
-          const uint32_t fi = gr % Lay::SCALE_SLOTS;
-          wait_warp(bar(Lay::B_SC + fi), (gr / Lay::SCALE_SLOTS) & 1u, failed);
-          if (failed) break;
-          sc = base + Lay::SC_OFF + fi * kScaleSlotBytes + part * 64;
-          mx = scaled_max32<BSC>(s0, ck0, lim, sl2, sc);
-          mx = fmaxf(mx, scaled_max32<BSC>(s1, ck0 + 32, lim, sl2, sc + 32));
-        } else {
-          mx = fmaxf(masked_max32(s0, ck0, lim), masked_max32(s1, ck0 + 32, lim));
-        }
+        const float mx = fmaxf(masked_max32(s0, ck0, lim), masked_max32(s1, ck0 + 32, lim));
         const float mo = exchange(mx);
         if (failed) break;
-        const float cm = BSC ? fmaxf(mx, mo) : __fmul_rn(sl2, fmaxf(mx, mo));
+        const float cm = __fmul_rn(sl2, fmaxf(mx, mo));
         const bool grow = cm > -INFINITY && (m_used == -INFINITY || __fsub_rn(cm, m_used) > kRescaleLog2);
         float alpha = 1.f;
         if (grow) {
@@ -1950,19 +1489,6 @@ __global__ void __launch_bounds__(kWideThreads, 1)
         const float ms = m_used == -INFINITY ? 0.f : m_used;
         float sum = 0.f;
         constexpr uint32_t PSTEP = SPLIT ? 16 : 8;
-        if constexpr (BSC != 0) {
-          const bool exact = __any_sync(FULL, fabsf(ms) > 4096.f || sl2 != 1.f);
-#pragma unroll 1
-          for (int ks = 0; ks < 4; ++ks) {
-            const float4 c = ld_scales(sc + 16 * ks);
-            uint32_t t[16];
-            tmem_ld16_wait(sp + 16 * ks, t);
-            if (exact)
-              probs16_scaled_store<BSC, true>(t, ck0 + 16 * ks, lim, sl2, ms, sum, sp + 8 * ks, c);
-            else
-              probs16_scaled_store<BSC, false>(t, ck0 + 16 * ks, lim, sl2, ms, sum, sp + 8 * ks, c);
-          }
-        } else {
         if (__any_sync(FULL, fabsf(ms) > 4096.f)) {
           probs16_store<M, true, SPLIT>(s0, ck0, lim, sl2, ms, sum, sp);
           probs16_store<M, true, SPLIT>(s0 + 16, ck0 + 16, lim, sl2, ms, sum, sp + PSTEP);
@@ -1977,7 +1503,6 @@ __global__ void __launch_bounds__(kWideThreads, 1)
         } else {
           probs16_store<M, false, SPLIT>(s1, ck0 + 32, lim, sl2, ms, sum, sp + 2 * PSTEP);
           probs16_store<M, false, SPLIT>(s1 + 16, ck0 + 48, lim, sl2, ms, sum, sp + 3 * PSTEP);
-        }
         }
         // O holds P V(0 .. kt-1) once P V(kt-1) completes (S(kt) may have been
         // issued before it): wait for it only when O must be rescaled
@@ -2017,28 +1542,11 @@ __global__ void __launch_bounds__(kWideThreads, 1)
         const float inv = lt > 0.f ? p.out_scale / lt : 0.f;
         bf16 *dst = p.out + static_cast<int64_t>(cur.row0 + (row_valid ? qi : 0)) * p.num_heads * D +
                     static_cast<int64_t>(cur.kvh * G + g) * D;
-        float *pdst = nullptr;  // the row's partial, for a part of the tile's keys
-        if constexpr (BSC != 0) {
-          if (cur.slot >= 0) {
-            const int64_t prow = static_cast<int64_t>(cur.slot) * kPrefillTileRows128 + r;
-            pdst = p.part_o + prow * D;
-            if (part == 0 && row_valid) p.part_lse[prow] = lt != 0.f ? m_used + __log2f(lt) : -INFINITY;
-          }
-        }
 #pragma unroll 1
         for (int ch = part * 4; ch < part * 4 + 4; ++ch) {
           uint32_t t[32];
           tmem_ld32_wait(tmem + lane_off + Tm::O + ch * 32, t);
-          if (BSC && pdst) {
-            if (row_valid) {
-#pragma unroll
-              for (int c = 0; c < 8; ++c) {
-                const float *f = reinterpret_cast<const float *>(&t[4 * c]);
-                *reinterpret_cast<float4 *>(pdst + ch * 32 + 4 * c) =
-                    make_float4(f[0] * inv, f[1] * inv, f[2] * inv, f[3] * inv);
-              }
-            }
-          } else if (row_valid) {
+          if (row_valid) {
 #pragma unroll
             for (int c = 0; c < 4; ++c) {
               const float *f = reinterpret_cast<const float *>(&t[8 * c]);
@@ -2074,13 +1582,13 @@ __global__ void __launch_bounds__(kWideThreads, 1)
   if (warp == 0) tmem_dealloc(tmem, kTmemCols);
 }
 
-template <int D, int G, typename E, bool KV8, int BSC>
+template <int D, int G, typename E, bool KV8>
 cudaError_t launch_prefill_tiles(const CUtensorMap &kmap, const CUtensorMap &vmap, const CUtensorMap &vmapb,
                                  const TileParams &tp, int sm_count, cudaStream_t stream) {
   if constexpr (D == kWideD) {
     (void)vmapb;
     constexpr int smem = WideLayout::BYTES;
-    auto kern = prefill_tile_wide_kernel<G, E, KV8, BSC>;
+    auto kern = prefill_tile_wide_kernel<G, E, KV8>;
     cudaError_t err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (err != cudaSuccess) return err;
     err = cudaFuncSetAttribute(kern, cudaFuncAttributePreferredSharedMemoryCarveout, 100);
@@ -2092,7 +1600,7 @@ cudaError_t launch_prefill_tiles(const CUtensorMap &kmap, const CUtensorMap &vma
     return launch_pdl(kern, dim3(static_cast<unsigned>(grid)), dim3(kWideThreads), smem, stream, kmap, vmap, tp);
   } else {
     constexpr int smem = TcLayout<D>::REQUEST;
-    auto kern = prefill_tile_kernel<D, G, E, KV8, BSC>;
+    auto kern = prefill_tile_kernel<D, G, E, KV8>;
     cudaError_t err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (err != cudaSuccess) return err;
     err = cudaFuncSetAttribute(kern, cudaFuncAttributePreferredSharedMemoryCarveout, 100);
@@ -2106,19 +1614,15 @@ cudaError_t launch_prefill_tiles(const CUtensorMap &kmap, const CUtensorMap &vma
   }
 }
 
-#define PA_TILE_INST1(DD, GG, EE, K8, BS)                                                                  \
-  template cudaError_t launch_prefill_tiles<DD, GG, EE, K8, BS>(const CUtensorMap &, const CUtensorMap &,     \
-                                                                const CUtensorMap &, const TileParams &, int, \
-                                                                cudaStream_t);
+#define PA_TILE_INST1(DD, GG, EE, K8)                                                                   \
+  template cudaError_t launch_prefill_tiles<DD, GG, EE, K8>(const CUtensorMap &, const CUtensorMap &,     \
+                                                            const CUtensorMap &, const TileParams &, int, \
+                                                            cudaStream_t);
 #define PA_TILE_INST(DD, GG)                                                                              \
-  PA_TILE_INST1(DD, GG, ElemBf16, false, 0)                                                           \
-  PA_TILE_INST1(DD, GG, ElemFp16, false, 0)                                                           \
-  PA_TILE_INST1(DD, GG, ElemBf16, true, 0)                                                            \
-  PA_TILE_INST1(DD, GG, ElemFp16, true, 0)                                                            \
-  PA_TILE_INST1(DD, GG, ElemBf16, true, 8)                                                                \
-  PA_TILE_INST1(DD, GG, ElemFp16, true, 8)                                                                \
-  PA_TILE_INST1(DD, GG, ElemBf16, true, 16)                                                               \
-  PA_TILE_INST1(DD, GG, ElemFp16, true, 16)
+  PA_TILE_INST1(DD, GG, ElemBf16, false)                                                                  \
+  PA_TILE_INST1(DD, GG, ElemFp16, false)                                                                  \
+  PA_TILE_INST1(DD, GG, ElemBf16, true)                                                                   \
+  PA_TILE_INST1(DD, GG, ElemFp16, true)
 PA_TILE_INST(128, 1)
 PA_TILE_INST(128, 2)
 PA_TILE_INST(128, 4)
