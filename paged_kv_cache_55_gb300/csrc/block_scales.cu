@@ -25,7 +25,9 @@ namespace pa {
 
 namespace {
 
-constexpr int kScatterWarps = 16;  // per CTA, at most
+// Warps per CTA, at most: a lane holds its NV chunks of a block in registers
+constexpr int scatter_chunks(int head_dim, int block_size) { return (block_size * head_dim / 8 + 31) / 32; }
+constexpr int scatter_warps(int head_dim, int block_size) { return scatter_chunks(head_dim, block_size) > 8 ? 8 : 16; }
 constexpr int kMinScaleExp = -64;
 
 // Largest finite magnitude of a 16-bit pair, bit pattern per half (magnitudes
@@ -118,9 +120,9 @@ __device__ __forceinline__ void find_request(const BlockScatterLaunch &p, int sh
 // a warp loads the block's new rows of its head into registers, reduces their
 // largest magnitude, and stores their codes.
 template <int D, int BS, typename E>
-__global__ void __launch_bounds__(kScatterWarps * 32) block_scatter_kernel(const BlockScatterLaunch p) {
+__global__ void __launch_bounds__(scatter_warps(D, BS) * 32) block_scatter_kernel(const BlockScatterLaunch p) {
   constexpr int CPR = D / 8;                   // 8-element chunks per row
-  constexpr int NV = (BS * CPR + 31) / 32;     // chunks per lane, at most
+  constexpr int NV = scatter_chunks(D, BS);    // chunks per lane, at most
   constexpr int SHIFT = BS == 8 ? 3 : (BS == 16 ? 4 : 5);
   __shared__ int4 s_found;
   griddep_wait();
@@ -184,10 +186,23 @@ __global__ void __launch_bounds__(kScatterWarps * 32) block_scatter_kernel(const
     uint32_t m2 = 0;
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
-      m2 = __vmaxu2(m2, __vmaxu2(finite_magnitudes<E>(x[j].x), finite_magnitudes<E>(x[j].y)));
-      m2 = __vmaxu2(m2, __vmaxu2(finite_magnitudes<E>(x[j].z), finite_magnitudes<E>(x[j].w)));
+      m2 = __vmaxu2(m2, __vmaxu2(x[j].x & 0x7FFF7FFFu, x[j].y & 0x7FFF7FFFu));
+      m2 = __vmaxu2(m2, __vmaxu2(x[j].z & 0x7FFF7FFFu, x[j].w & 0x7FFF7FFFu));
     }
-    const uint32_t m = __reduce_max_sync(0xffffffffu, max(m2 & 0xffffu, m2 >> 16));
+    uint32_t m = __reduce_max_sync(0xffffffffu, max(m2 & 0xffffu, m2 >> 16));
+    if (m >= (E::kUmmaFormat ? 0x7F80u : 0x7C00u)) {  // an infinity or NaN among them: the finite ones alone
+      m2 = 0;
+#pragma unroll 1
+      for (int j = 0; j < NV; ++j) {
+        const int k = lane + 32 * j;
+        if (k < n) {
+          const uint4 v = ld_cg(src + k / CPR * stride8 + k % CPR);
+          m2 = __vmaxu2(m2, __vmaxu2(finite_magnitudes<E>(v.x), finite_magnitudes<E>(v.y)));
+          m2 = __vmaxu2(m2, __vmaxu2(finite_magnitudes<E>(v.z), finite_magnitudes<E>(v.w)));
+        }
+      }
+      m = __reduce_max_sync(0xffffffffu, max(m2 & 0xffffu, m2 >> 16));
+    }
     // a scale that is no positive finite number (never written) counts as 0
     if (!(before > 0.f && before <= 3.4028234e38f)) before = 0.f;
     const float after = fmaxf(before, needed_scale(E::lo(m)));
@@ -217,7 +232,8 @@ template <int D, int BS, typename E>
 cudaError_t launch_scatter(const BlockScatterLaunch &p, cudaStream_t stream) {
   const int64_t units =
       p.max_query_len <= 1 ? p.num_seqs : p.total_q / BS + 2 * static_cast<int64_t>(p.num_seqs);
-  const int warps = 2 * p.num_kv_heads < kScatterWarps ? 2 * p.num_kv_heads : kScatterWarps;
+  constexpr int most = scatter_warps(D, BS);
+  const int warps = 2 * p.num_kv_heads < most ? 2 * p.num_kv_heads : most;
   return launch_pdl(block_scatter_kernel<D, BS, E>, dim3(static_cast<unsigned>(units)), dim3(warps * 32), 0, stream,
                     p);
 }

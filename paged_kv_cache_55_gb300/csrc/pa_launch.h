@@ -60,7 +60,6 @@ struct NormRopeLaunch {
   int32_t dst;  // 0 K rows, 1 16-bit caches, 2 E4M3 caches with one scale each
   float k_scale, v_scale;
   int32_t dtype;
-  int32_t slices;  // warps per token (set by the launcher)
   unsigned int *status;
 };
 cudaError_t launch_norm_rope(const NormRopeLaunch &p, int sm_count, cudaStream_t stream);
