@@ -153,33 +153,38 @@ struct MergeParams {
 
 // ---- planning --------------------------------------------------------------
 
-// Exclusive scan over a block of NT threads (at most 1024); *total: the sum.
-template <int NT>
-__device__ __forceinline__ unsigned long long block_scan(unsigned long long v, unsigned long long *warp_tot,
-                                                         unsigned long long *total) {
+// Exclusive scans of N values over a block of NT threads (at most 1024) with
+// one barrier: every warp scans the warps' totals for itself. total: the sums.
+// `warp_tot` is this scan's own array.
+template <int NT, int N>
+__device__ __forceinline__ void block_scan(const unsigned long long (&v)[N], unsigned long long (*warp_tot)[32],
+                                           unsigned long long (&before)[N], unsigned long long (&total)[N]) {
   constexpr int NWARP = NT / 32;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  unsigned long long incl = v;
+  unsigned long long incl[N];
 #pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const unsigned long long t = __shfl_up_sync(0xffffffffu, incl, o);
-    if (lane >= o) incl += t;
-  }
-  __syncthreads();  // warp_tot of the previous scan has been read
-  if (lane == 31) warp_tot[warp] = incl;
-  __syncthreads();
-  if (warp == 0) {
-    unsigned long long t = lane < NWARP ? warp_tot[lane] : 0;
+  for (int k = 0; k < N; ++k) {
+    incl[k] = v[k];
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
+      const unsigned long long t = __shfl_up_sync(0xffffffffu, incl[k], o);
+      if (lane >= o) incl[k] += t;
+    }
+    if (lane == 31) warp_tot[k][warp] = incl[k];
+  }
+  __syncthreads();
+#pragma unroll
+  for (int k = 0; k < N; ++k) {
+    unsigned long long t = lane < NWARP ? warp_tot[k][lane] : 0;
+#pragma unroll
+    for (int o = 1; o < NWARP; o <<= 1) {
       const unsigned long long u = __shfl_up_sync(0xffffffffu, t, o);
       if (lane >= o) t += u;
     }
-    if (lane < NWARP) warp_tot[lane] = t;
+    total[k] = __shfl_sync(0xffffffffu, t, NWARP - 1);
+    const unsigned long long below = __shfl_sync(0xffffffffu, t, warp > 0 ? warp - 1 : 0);
+    before[k] = (warp > 0 ? below : 0) + incl[k] - v[k];
   }
-  __syncthreads();
-  *total = warp_tot[NWARP - 1];
-  return (warp > 0 ? warp_tot[warp - 1] : 0) + incl - v;
 }
 
 struct Request {
@@ -228,64 +233,54 @@ __device__ __forceinline__ int find_range(const int *pre, int n, int i) {
   return lo;
 }
 
-// One CTA. Three sweeps over the requests (the lengths stay in registers when
-// NT threads cover them): the tiles of all decode requests, hence the unit
-// size U; the number of full units, whose items come first in the queue; then
-// the items, each request's key_tiles / U full ones and one of the remainder,
-// written by all threads (a thread finds an item's request in the prefix sums).
+// One CTA. Sweeps over the requests (one read of the lengths when NT threads
+// cover them): the tiles of all decode requests, hence the unit size U, and the
+// prefill tiles with their key ranges, hence their parts; the number of full
+// units, whose items come first in the queue; then the items, each request's
+// key_tiles / U full ones and one of the remainder, written by all threads (a
+// thread finds an item's request in the prefix sums).
 // Item: {b, first query row, rows, position of the first}, {key begin, key
 // end, partition (-1: the whole range), partitions}.
 template <int NT>
 __global__ void __launch_bounds__(NT) block_plan_kernel(const PlanParams p) {
-  __shared__ unsigned long long warp_tot[32];
+  constexpr int kCountShift = 40;  // a count above 40 bits of tiles
+  constexpr unsigned long long kLow = (1ull << kCountShift) - 1;
+  __shared__ unsigned long long sum_tot[3][32], full_tot[1][32], scan_tot[2][32];
   __shared__ int pre_full[NT + 1], pre_tile[NT + 1], s_q0[NT], s_ql[NT], s_len[NT];
   const int tid = threadIdx.x;
   griddep_wait();
   griddep_launch_dependents();
   const bool once = p.num_seqs <= NT;
-  Request r{};
-  unsigned long long mine = 0, total;  // key tiles, and decode requests in the top 24 bits
-  for (int b = tid; b < p.num_seqs; b += NT) {
-    r = read_request(p, b, true);
-    mine += static_cast<unsigned long long>(r.key_tiles) | (r.key_tiles > 0 ? 1ull << 40 : 0);
-  }
-  block_scan<NT>(mine, warp_tot, &total);
-  const int64_t U64 = unit_tiles(static_cast<int64_t>(total & ((1ull << 40) - 1)) * p.num_kv_heads,
-                                 static_cast<int64_t>(total >> 40) * p.num_kv_heads, p.warps);
-  const int U = U64 > (1 << 24) ? (1 << 24) : static_cast<int>(U64);
-  const int unit_keys = U * kTile;
-  mine = 0;
-  for (int b = tid; b < p.num_seqs; b += NT) {
-    if (!once) r = read_request(p, b, false);
-    mine += r.key_tiles / U;
-  }
-  unsigned long long full_total;
-  block_scan<NT>(mine, warp_tot, &full_total);
-  const int all_full = static_cast<int>(min(full_total, static_cast<unsigned long long>(p.max_items)));
-  // parts of the prefill tiles
   const bool chunks = p.max_query_len > p.rows_per_item;
-  int split = kNoSplit;  // ranges per part
+  const int most_split = chunks && p.max_part_items > 0 ? part_items(p.num_kv_heads) * 3 / 4 : 0;  // tiles
   auto tile_ranges = [&](int len, int ql, int t) {  // 128-key ranges that tile t of a request walks
     return (len - ql + min((t + 1) * p.tile_pos, ql) - 1) / kRangeKeys + 1;
   };
-  if (chunks && p.max_part_items > 0) {
-    unsigned long long tiles, ranges;
-    mine = 0;
-    for (int b = tid; b < p.num_seqs; b += NT) {
-      if (!once) r = read_request(p, b, false);
-      mine += r.tiles;
-    }
-    block_scan<NT>(mine, warp_tot, &tiles);
-    if (tiles > 0 && tiles * 4 <= static_cast<unsigned long long>(part_items(p.num_kv_heads)) * 3) {
-      mine = 0;
-      for (int b = tid; b < p.num_seqs; b += NT) {
-        if (!once) r = read_request(p, b, false);
-        for (int t = 0; t < r.tiles; ++t) mine += tile_ranges(r.len, r.ql, t);
-      }
-      block_scan<NT>(mine, warp_tot, &ranges);
-      split = part_ranges(static_cast<int64_t>(tiles), static_cast<int64_t>(ranges), p.num_kv_heads);
-    }
+  Request r{};
+  // decode key tiles and, above them, decode requests; prefill tiles; their ranges
+  unsigned long long mine[3] = {0, 0, 0}, total[3], unused[3];
+  for (int b = tid; b < p.num_seqs; b += NT) {
+    r = read_request(p, b, true);
+    mine[0] += static_cast<unsigned long long>(r.key_tiles) | (r.key_tiles > 0 ? 1ull << kCountShift : 0);
+    mine[1] += r.tiles;
+    if (r.tiles <= most_split)
+      for (int t = 0; t < r.tiles; ++t) mine[2] += tile_ranges(r.len, r.ql, t);
   }
+  block_scan<NT>(mine, sum_tot, unused, total);
+  const int64_t U64 = unit_tiles(static_cast<int64_t>(total[0] & kLow) * p.num_kv_heads,
+                                 static_cast<int64_t>(total[0] >> kCountShift) * p.num_kv_heads, p.warps);
+  const int U = U64 > (1 << 24) ? (1 << 24) : static_cast<int>(U64);
+  const int unit_keys = U * kTile;
+  int split = kNoSplit;  // ranges per part
+  if (total[1] > 0 && total[1] <= static_cast<unsigned long long>(most_split))
+    split = part_ranges(static_cast<int64_t>(total[1]), static_cast<int64_t>(total[2]), p.num_kv_heads);
+  unsigned long long full_total[1] = {0};
+  if (!once) {
+    unsigned long long full[1] = {0}, none[1];
+    for (int b = tid; b < p.num_seqs; b += NT) full[0] += read_request(p, b, false).key_tiles / U;
+    block_scan<NT>(full, full_tot, none, full_total);
+  }
+  int all_full = static_cast<int>(min(full_total[0], static_cast<unsigned long long>(p.max_items)));
   int carry_full = 0, carry_rest = 0, carry_tile = 0;
   for (int base = 0; base < p.num_seqs; base += NT) {
     const int b = base + tid, n = min(NT, p.num_seqs - base);
@@ -295,21 +290,20 @@ __global__ void __launch_bounds__(NT) block_plan_kernel(const PlanParams p) {
     }
     if (b >= p.num_seqs) r = Request{};
     const int full = r.key_tiles / U, rest = r.key_tiles % U ? 1 : 0;
-    unsigned long long tot, tile_tot;
-    const unsigned long long ex =
-        block_scan<NT>(static_cast<unsigned long long>(full) | (static_cast<unsigned long long>(rest) << 40), warp_tot,
-                       &tot);
-    unsigned long long ex_tile = 0;
-    tile_tot = 0;
-    if (chunks) {
-      unsigned long long n_parts = r.tiles;
-      if (split != kNoSplit) {
-        n_parts = 0;
-        for (int t = 0; t < r.tiles; ++t) n_parts += (tile_ranges(r.len, r.ql, t) + split - 1) / split;
-      }
-      ex_tile = block_scan<NT>(n_parts, warp_tot, &tile_tot);
+    unsigned long long counts[2], ex2[2], tot2[2];
+    counts[0] = static_cast<unsigned long long>(full) | (static_cast<unsigned long long>(rest) << kCountShift);
+    counts[1] = r.tiles;
+    if (split != kNoSplit) {
+      counts[1] = 0;
+      for (int t = 0; t < r.tiles; ++t) counts[1] += (tile_ranges(r.len, r.ql, t) + split - 1) / split;
     }
-    const int ex_full = static_cast<int>(ex & ((1ull << 40) - 1)), n_full = static_cast<int>(tot & ((1ull << 40) - 1));
+    block_scan<NT>(counts, scan_tot, ex2, tot2);
+    const unsigned long long ex = ex2[0], tot = tot2[0], ex_tile = ex2[1], tile_tot = tot2[1];
+    if (once) {
+      full_total[0] = tot & kLow;
+      all_full = static_cast<int>(min(full_total[0], static_cast<unsigned long long>(p.max_items)));
+    }
+    const int ex_full = static_cast<int>(ex & kLow), n_full = static_cast<int>(tot & kLow);
     const int n_tile = static_cast<int>(tile_tot);
     pre_full[tid] = ex_full;
     pre_tile[tid] = static_cast<int>(ex_tile);
@@ -317,7 +311,7 @@ __global__ void __launch_bounds__(NT) block_plan_kernel(const PlanParams p) {
     s_ql[tid] = r.ql;
     s_len[tid] = r.len;
     if (b < p.num_seqs) {
-      const int item = all_full + carry_rest + static_cast<int>(ex >> 40);
+      const int item = all_full + carry_rest + static_cast<int>(ex >> kCountShift);
       p.nparts[b] = full + rest;
       p.first_full[b] = carry_full + ex_full;
       p.rest[b] = rest ? item : -1;
@@ -363,13 +357,13 @@ __global__ void __launch_bounds__(NT) block_plan_kernel(const PlanParams p) {
                     : make_int4(0, end, -1, 1);
     }
     carry_full += n_full;
-    carry_rest += static_cast<int>(tot >> 40);
+    carry_rest += static_cast<int>(tot >> kCountShift);
     carry_tile += n_tile;
-    __syncthreads();  // the prefix arrays are free for the next sweep
+    __syncthreads();  // the prefix arrays and scan_tot are free for the next sweep
   }
   if (tid == 0) {
     int items = all_full + carry_rest;
-    if (static_cast<unsigned long long>(carry_rest) + full_total > static_cast<unsigned long long>(p.max_items)) {
+    if (static_cast<unsigned long long>(carry_rest) + full_total[0] > static_cast<unsigned long long>(p.max_items)) {
       flag_error(p.status, PA_FLAG_LENGTHS);
       items = p.max_items;
     }
