@@ -581,24 +581,36 @@ __global__ void __launch_bounds__(kTileThreads8, 1)
       ++nx;
     };
     const int ch0 = part ? (NCH + 1) / 2 : 0, ch1 = part ? NCH : (NCH + 1) / 2;  // this warp's O chunks
+    // the factors of this warp's 32 rows, from the lanes that stored their Q
+    // (lane l < 16: row 16 part + l); the values exchanged before have been read
+    auto row_factors = [&](float mine) -> float {
+      if (lane < 16) xch[(h * kParts + part) * kHalfRows + quad * 32 + part * 16 + lane] = mine;
+      pair_sync();
+      const float v = xch[(h * kParts + (lane >> 4)) * kHalfRows + r];
+      pair_sync();
+      return v;
+    };
     const int g = r % G;
     uint32_t phh = 0;  // ranges this half has run so far
     uint32_t gvs = 0;  // ranges of the CTA's earlier units (both halves)
 
-    // Q of the half for unit `u`: this warp stores its half of the row's 16-byte
-    // chunks (row r = (position, head), K-major, swizzled); returns the row's
-    // softmax factor (log2 domain, times 2^e for a scaled bf16 row over 8-bit caches)
+    // Q of the half for unit `u`: this warp stores 16 of its 32
+    // rows (row r = (position, head), K-major, swizzled), consecutive lanes
+    // consecutive 16-byte chunks, and returns (lanes 0..15) the softmax factor of row 16 part + lane: 2^e,
+    // e > 0 for a scaled bf16 row. Measured
+    // (16 chunks of 512, 6.7 tiles a CTA): a lane per row instead, 32 lines an
+    // instruction, cost 36000 cycles between two tiles.
     auto load_q = [&](const TileUnit &u) -> float {
-      const int qi = h * POS_PER_HALF + r / G;
-      const bool valid = qi < u.npos;
       const uint32_t sQ = sQ0 + h * Lay::Q_BYTES;
-      const bf16 *qrow =
-          p.q + static_cast<int64_t>(u.row0 + (valid ? qi : 0)) * p.q_stride + static_cast<int64_t>(u.kvh * G + g) * D;
+      const int row_w = quad * 32 + part * 16;  // this warp's first row
       // q is only required to be 4-byte aligned: 16-byte loads when rows allow them
       const bool q16 = (reinterpret_cast<uintptr_t>(p.q) & 15u) == 0 && (p.q_stride & 7) == 0;
-      auto ldq = [&](int c) {
+      auto ldq = [&](int row, int c) {
         uint4 w = make_uint4(0u, 0u, 0u, 0u);
-        if (valid) {
+        const int qi = h * POS_PER_HALF + row / G;
+        if (qi < u.npos) {
+          const bf16 *qrow = p.q + static_cast<int64_t>(u.row0 + qi) * p.q_stride +
+                             static_cast<int64_t>(u.kvh * G + row % G) * D;
           if (q16) {
             w = __ldg(reinterpret_cast<const uint4 *>(qrow) + c);
           } else {
@@ -608,37 +620,54 @@ __global__ void __launch_bounds__(kTileThreads8, 1)
         }
         return w;
       };
-      float rowf = 1.f;  // > 0: the max of raw scores gives the max of scaled ones
-      float qmul = 1.f;
-      if constexpr (std::is_same<E, ElemBf16>::value) {
-        // bf16 rows over 8-bit caches: 2^-e, e > 0 only when the row's largest |q| reaches 2^15
-        float amax = 0.f;
-#pragma unroll 4
-        for (int c = 0; c < D / 8; ++c) {
-          const uint4 w = ldq(c);
-          const uint32_t v[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-          for (int k = 0; k < 4; ++k)
-            amax = fmaxf(amax, fmaxf(fabsf(ElemBf16::lo(v[k])), fabsf(ElemBf16::hi(v[k]))));
-        }
-        const int ex = static_cast<int>((__float_as_uint(amax) >> 23) & 0xffu) - 127;  // floor(log2(amax))
-        const int e = ex >= 15 ? min(ex - 14, 120) : 0;
-        qmul = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
-        rowf = __uint_as_float(static_cast<uint32_t>(127 + e) << 23);
-      }
-      constexpr int CQ = D / 16;  // chunks per warp (D / 8 per row)
-#pragma unroll 4
-      for (int c = part * CQ; c < (part + 1) * CQ; ++c) {
-        uint4 w = ldq(c);
+      auto stq = [&](int row, int c, uint4 w, float qmul) {
         if constexpr (std::is_same<E, ElemBf16>::value) {
           w = make_uint4(ElemFp16::pack(ElemBf16::lo(w.x) * qmul, ElemBf16::hi(w.x) * qmul),
                          ElemFp16::pack(ElemBf16::lo(w.y) * qmul, ElemBf16::hi(w.y) * qmul),
                          ElemFp16::pack(ElemBf16::lo(w.z) * qmul, ElemBf16::hi(w.z) * qmul),
                          ElemFp16::pack(ElemBf16::lo(w.w) * qmul, ElemBf16::hi(w.w) * qmul));
         }
-        asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};\n" ::"r"(sQ + Lay::off(r, c, Lay::Q_ATOM)), "r"(w.x),
+        asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};\n" ::"r"(sQ + Lay::off(row, c, Lay::Q_ATOM)), "r"(w.x),
                      "r"(w.y), "r"(w.z), "r"(w.w)
                      : "memory");
+      };
+      constexpr int CPR = D / 8, NL = 16 * CPR / 32;  // chunks per row, and per lane
+      uint4 w[NL];
+#pragma unroll
+      for (int i = 0; i < NL; ++i) w[i] = ldq(row_w + (32 * i + lane) / CPR, (32 * i + lane) % CPR);
+      bool large = false;
+      float rowf = 1.f;
+      if constexpr (std::is_same<E, ElemBf16>::value) {
+        // an element of magnitude 2^15 or more (or NaN) that fp16 may not hold
+        uint32_t m = 0;
+#pragma unroll
+        for (int i = 0; i < NL; ++i) {
+          m = __vimax3_u16x2(m, w[i].x & 0x7FFF7FFFu, w[i].y & 0x7FFF7FFFu);
+          m = __vimax3_u16x2(m, w[i].z & 0x7FFF7FFFu, w[i].w & 0x7FFF7FFFu);
+        }
+        large = __any_sync(FULL, max(m & 0xffffu, m >> 16) >= 0x4700u);  // bf16 2^15
+      }
+      if (!large) {
+#pragma unroll
+        for (int i = 0; i < NL; ++i) stq(row_w + (32 * i + lane) / CPR, (32 * i + lane) % CPR, w[i], 1.f);
+      } else if (lane < 16) {  // rare: a lane per row
+        const int row = row_w + lane;
+        // 2^-e, e > 0 only when the row's largest |q| reaches 2^15
+        float amax = 0.f;
+#pragma unroll 1
+        for (int c = 0; c < CPR; ++c) {
+          const uint4 x = ldq(row, c);
+          const uint32_t v[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            amax = fmaxf(amax, fmaxf(fabsf(ElemBf16::lo(v[k])), fabsf(ElemBf16::hi(v[k]))));
+        }
+        const int ex = static_cast<int>((__float_as_uint(amax) >> 23) & 0xffu) - 127;  // floor(log2(amax))
+        const int e = ex >= 15 ? min(ex - 14, 120) : 0;
+        const float qmul = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
+#pragma unroll 1
+        for (int c = 0; c < CPR; ++c) stq(row, c, ldq(row, c), qmul);
+        rowf = __uint_as_float(static_cast<uint32_t>(127 + e) << 23);
       }
       fence_proxy_async_smem();  // the MMA reads Q through the async proxy
       __syncwarp();
@@ -648,8 +677,9 @@ __global__ void __launch_bounds__(kTileThreads8, 1)
 
     TileUnit cur;
     read_unit(0, cur);
-    float rowf = 1.f;  // the row's score factor: 2^e for a scaled bf16 row
-    if (!failed && !cur.stop) rowf = load_q(cur);
+    // the row's score factor (> 0: the max of raw scores gives the max of scaled ones)
+    float rowf = 1.f;
+    if (!failed && !cur.stop) rowf = row_factors(load_q(cur));
     for (uint32_t j = 0; !failed && !cur.stop; ++j) {
       int nkt_h[kHalves];
       const int nkt_all = ranges(cur, nkt_h);
@@ -737,12 +767,12 @@ __global__ void __launch_bounds__(kTileThreads8, 1)
       }
       if (failed) break;
       // the next unit's record and Q (overlapping this unit's last products)
+      float next_mine = 1.f;
       TileUnit nxt;
       read_unit(j + 1, nxt);
-      float nrowf = rowf;
       if (!failed && !nxt.stop) {
         wait_warp(bar(Lay::B_QE + h), j & 1u, failed);  // the MMA warp has taken this unit's Q
-        if (!failed) nrowf = load_q(nxt);
+        if (!failed) next_mine = load_q(nxt);
       }
       if (failed) break;
       if (nk > 0) {
@@ -795,8 +825,8 @@ __global__ void __launch_bounds__(kTileThreads8, 1)
       }
       phh += nk;
       gvs += nkt_all;
+      if (!nxt.stop) rowf = row_factors(next_mine);
       cur = nxt;
-      rowf = nrowf;
     }
   }
 
