@@ -908,11 +908,14 @@ struct Merged {
   }
 };
 
-constexpr int kTileMergeCtas = 8;  // CTAs that share the rows of one split prefill tile
+// CTAs of NW warps that merge a part's share (half at most) of a split prefill
+// tile's rows, a warp per row
+template <int D, int NW>
+constexpr int kTileMergeCtas = prefill_tile_rows(D) / 2 / NW;
 
 template <int D, int G, typename E, int NW>
 __global__ void __launch_bounds__(NW * 32) block_merge_kernel(const MergeParams p) {
-  constexpr int EPL = Merged<D>::EPL;
+  constexpr int EPL = Merged<D>::EPL, CTAS = kTileMergeCtas<D, NW>;
   __shared__ float s_m[NW], s_w[NW], s_acc[NW][32 * EPL];
   griddep_wait();
   griddep_launch_dependents();
@@ -920,8 +923,8 @@ __global__ void __launch_bounds__(NW * 32) block_merge_kernel(const MergeParams 
   const int pairs = p.num_seqs * p.num_kv_heads;
   if (static_cast<int>(blockIdx.x) >= pairs) {
     // a split prefill tile: a warp per row
-    const int i = blockIdx.x - pairs, item = i / (p.num_kv_heads * kTileMergeCtas);
-    const int kvh = (i / kTileMergeCtas) % p.num_kv_heads, rb = i % kTileMergeCtas;
+    const int i = blockIdx.x - pairs, item = i / (p.num_kv_heads * CTAS);
+    const int kvh = (i / CTAS) % p.num_kv_heads, rb = i % CTAS;
     if (item >= min(ld_cg(p.tile_count), p.tile_items)) return;
     const int4 r0 = ld_cg(p.tiles + 2 * item), r1 = ld_cg(p.tiles + 2 * item + 1);
     const int row0 = r0.y, npos = r0.z, parts = r1.w;
@@ -931,7 +934,7 @@ __global__ void __launch_bounds__(NW * 32) block_merge_kernel(const MergeParams 
     if (parts <= 1 || part < 0 || part >= parts || first < 0 || first + parts > p.tile_items) return;
     if (row0 < 0 || npos < 1 || npos * G > ROWS || row0 + npos > p.total_q) return;
     const int row_end = npos * G * (part + 1) / parts;
-    for (int row = npos * G * part / parts + rb * NW + warp; row < row_end; row += kTileMergeCtas * NW) {
+    for (int row = npos * G * part / parts + rb * NW + warp; row < row_end; row += CTAS * NW) {
       Merged<D> m;
       m.add(0, parts, lane, p.tile_lse, p.tile_o, [&](int k) {
         return (static_cast<int64_t>(first + k) * p.num_kv_heads + kvh) * ROWS + row;
@@ -1150,11 +1153,13 @@ cudaError_t launch_typed(const AttnLaunch &a, const BlockWorkspace &w, cudaStrea
     mp.part_lse = dp.part_lse;
     mp.out = dp.out;
     const unsigned pairs = static_cast<unsigned>(a.num_seqs * a.num_kv_heads);
-    const unsigned ctas = pairs + static_cast<unsigned>(mp.tile_items * a.num_kv_heads * kTileMergeCtas);
+    const unsigned part_pairs = static_cast<unsigned>(mp.tile_items * a.num_kv_heads);
     if (pairs <= 2u * static_cast<unsigned>(a.sm_count))
-      err = launch_pdl(block_merge_kernel<D, G, E, 16>, dim3(ctas), dim3(16 * 32), 0, stream, mp);
+      err = launch_pdl(block_merge_kernel<D, G, E, 16>, dim3(pairs + part_pairs * kTileMergeCtas<D, 16>), dim3(16 * 32),
+                       0, stream, mp);
     else
-      err = launch_pdl(block_merge_kernel<D, G, E, 4>, dim3(ctas), dim3(4 * 32), 0, stream, mp);
+      err = launch_pdl(block_merge_kernel<D, G, E, 4>, dim3(pairs + part_pairs * kTileMergeCtas<D, 4>), dim3(4 * 32), 0,
+                       stream, mp);
     if (err != cudaSuccess) return err;
     ++*launched;
   }

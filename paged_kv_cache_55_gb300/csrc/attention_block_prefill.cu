@@ -291,6 +291,7 @@ __global__ void __launch_bounds__(kTileThreads8, 1)
     const int total_units = min(max(ld_cg(p.tile_count), 0), p.max_tiles) * Hkv;
     const int box_rows = bs < kRawBoxRows ? bs : kRawBoxRows;
     const int nbk = kKeyTile / box_rows;                // 4 .. 16
+    constexpr int LINES = (G * D * 2 + 127) / 128;      // of a position's q heads
     uint32_t j = 0, g = 0;
     for (;;) {
       int u = 0;
@@ -336,6 +337,14 @@ __global__ void __launch_bounds__(kTileThreads8, 1)
       __syncwarp();
       ++j;
       if (r.stop) break;
+      // its q rows towards L2, ahead of the softmax warps that load them: a
+      // position's G heads are contiguous
+      for (int i = lane; i < r.npos * LINES; i += 32) {
+        const int pos = i / LINES;
+        const char *row = reinterpret_cast<const char *>(p.q + static_cast<int64_t>(r.row0 + pos) * p.q_stride +
+                                                         static_cast<int64_t>(r.kvh * G) * D);
+        asm volatile("prefetch.global.L2 [%0];\n" ::"l"(row + (i - pos * LINES) * 128));
+      }
       const int32_t *table = p.block_tables + static_cast<int64_t>(r.b) * p.max_blocks_per_seq;
       // First cache row of the box of `rows` keys starting at `key`: a block-table
       // lookup (block sizes are powers of two); keys past the end, or a block id
@@ -594,6 +603,10 @@ __global__ void __launch_bounds__(kTileThreads8, 1)
     uint32_t phh = 0;  // ranges this half has run so far
     uint32_t gvs = 0;  // ranges of the CTA's earlier units (both halves)
 
+    auto q_row = [&](const TileUnit &u, int row) {
+      return p.q + static_cast<int64_t>(u.row0 + h * POS_PER_HALF + row / G) * p.q_stride +
+             static_cast<int64_t>(u.kvh * G + row % G) * D;
+    };
     // Q of the half for unit `u`: this warp stores 16 of its 32
     // rows (row r = (position, head), K-major, swizzled), consecutive lanes
     // consecutive 16-byte chunks, and returns (lanes 0..15) the softmax factor of row 16 part + lane: 2^e,
@@ -607,10 +620,8 @@ __global__ void __launch_bounds__(kTileThreads8, 1)
       const bool q16 = (reinterpret_cast<uintptr_t>(p.q) & 15u) == 0 && (p.q_stride & 7) == 0;
       auto ldq = [&](int row, int c) {
         uint4 w = make_uint4(0u, 0u, 0u, 0u);
-        const int qi = h * POS_PER_HALF + row / G;
-        if (qi < u.npos) {
-          const bf16 *qrow = p.q + static_cast<int64_t>(u.row0 + qi) * p.q_stride +
-                             static_cast<int64_t>(u.kvh * G + row % G) * D;
+        if (h * POS_PER_HALF + row / G < u.npos) {
+          const bf16 *qrow = q_row(u, row);
           if (q16) {
             w = __ldg(reinterpret_cast<const uint4 *>(qrow) + c);
           } else {
@@ -634,40 +645,47 @@ __global__ void __launch_bounds__(kTileThreads8, 1)
       constexpr int CPR = D / 8, NL = 16 * CPR / 32;  // chunks per row, and per lane
       uint4 w[NL];
 #pragma unroll
-      for (int i = 0; i < NL; ++i) w[i] = ldq(row_w + (32 * i + lane) / CPR, (32 * i + lane) % CPR);
-      bool large = false;
+      for (int i = 0; i < NL; ++i) {
+        const int row = row_w + (32 * i + lane) / CPR, c = (32 * i + lane) % CPR;
+        w[i] = make_uint4(0u, 0u, 0u, 0u);
+        if (q16 && h * POS_PER_HALF + row / G < u.npos)
+          w[i] = __ldg(reinterpret_cast<const uint4 *>(q_row(u, row)) + c);
+      }
+      bool rare = !q16;  // or an element of magnitude 2^15 or more (or NaN) that fp16 may not hold
       float rowf = 1.f;
       if constexpr (std::is_same<E, ElemBf16>::value) {
-        // an element of magnitude 2^15 or more (or NaN) that fp16 may not hold
         uint32_t m = 0;
 #pragma unroll
         for (int i = 0; i < NL; ++i) {
           m = __vimax3_u16x2(m, w[i].x & 0x7FFF7FFFu, w[i].y & 0x7FFF7FFFu);
           m = __vimax3_u16x2(m, w[i].z & 0x7FFF7FFFu, w[i].w & 0x7FFF7FFFu);
         }
-        large = __any_sync(FULL, max(m & 0xffffu, m >> 16) >= 0x4700u);  // bf16 2^15
+        rare = rare || __any_sync(FULL, max(m & 0xffffu, m >> 16) >= 0x4700u);  // bf16 2^15
       }
-      if (!large) {
+      if (!rare) {
 #pragma unroll
         for (int i = 0; i < NL; ++i) stq(row_w + (32 * i + lane) / CPR, (32 * i + lane) % CPR, w[i], 1.f);
-      } else if (lane < 16) {  // rare: a lane per row
+      } else if (lane < 16) {  // a lane per row
         const int row = row_w + lane;
-        // 2^-e, e > 0 only when the row's largest |q| reaches 2^15
-        float amax = 0.f;
+        float qmul = 1.f;
+        if constexpr (std::is_same<E, ElemBf16>::value) {
+          // 2^-e, e > 0 only when the row's largest |q| reaches 2^15
+          float amax = 0.f;
 #pragma unroll 1
-        for (int c = 0; c < CPR; ++c) {
-          const uint4 x = ldq(row, c);
-          const uint32_t v[4] = {x.x, x.y, x.z, x.w};
+          for (int c = 0; c < CPR; ++c) {
+            const uint4 x = ldq(row, c);
+            const uint32_t v[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
-          for (int k = 0; k < 4; ++k)
-            amax = fmaxf(amax, fmaxf(fabsf(ElemBf16::lo(v[k])), fabsf(ElemBf16::hi(v[k]))));
+            for (int k = 0; k < 4; ++k)
+              amax = fmaxf(amax, fmaxf(fabsf(ElemBf16::lo(v[k])), fabsf(ElemBf16::hi(v[k]))));
+          }
+          const int ex = static_cast<int>((__float_as_uint(amax) >> 23) & 0xffu) - 127;  // floor(log2(amax))
+          const int e = ex >= 15 ? min(ex - 14, 120) : 0;
+          qmul = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
+          rowf = __uint_as_float(static_cast<uint32_t>(127 + e) << 23);
         }
-        const int ex = static_cast<int>((__float_as_uint(amax) >> 23) & 0xffu) - 127;  // floor(log2(amax))
-        const int e = ex >= 15 ? min(ex - 14, 120) : 0;
-        const float qmul = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
 #pragma unroll 1
         for (int c = 0; c < CPR; ++c) stq(row, c, ldq(row, c), qmul);
-        rowf = __uint_as_float(static_cast<uint32_t>(127 + e) << 23);
       }
       fence_proxy_async_smem();  // the MMA reads Q through the async proxy
       __syncwarp();
