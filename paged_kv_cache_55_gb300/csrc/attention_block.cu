@@ -841,14 +841,14 @@ struct Merged {
 #pragma unroll
     for (int e = 0; e < EPL; ++e) acc[e] = 0.f;
   }
-  // partitions [begin, end): row at(k) of o and lse; a partition without keys
+  // partitions [begin, end), J at a time: row at(k) of o and lse; a partition without keys
   // (lse -inf) is left out, whatever its outputs hold
-  template <typename At>
+  template <int J, typename At>
   __device__ __forceinline__ void add(int begin, int end, int lane, const float *lse, const float *o, At at) {
-    for (int k0 = begin; k0 < end; k0 += 8) {
-      float lv[8], ov[8][EPL];
+    for (int k0 = begin; k0 < end; k0 += J) {
+      float lv[J], ov[J][EPL];
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
+      for (int j = 0; j < J; ++j) {
         const int64_t row = at(min(k0 + j, end - 1));
         lv[j] = ld_cg(lse + row);
         const float *src = o + row * D + lane * EPL;
@@ -868,7 +868,7 @@ struct Merged {
       }
       float Mn = M;
 #pragma unroll
-      for (int j = 0; j < 8; ++j)
+      for (int j = 0; j < J; ++j)
         if (k0 + j < end) Mn = fmaxf(Mn, lv[j]);
       const float Ms = Mn == -INFINITY ? 0.f : Mn;
       const float r = ex2_approx(M - Ms);
@@ -877,7 +877,7 @@ struct Merged {
       for (int e = 0; e < EPL; ++e) acc[e] *= r;
       M = Mn;
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
+      for (int j = 0; j < J; ++j) {
         if (k0 + j < end && lv[j] != -INFINITY) {
           const float w = ex2_approx(lv[j] - Ms);
           wsum += w;
@@ -936,9 +936,11 @@ __global__ void __launch_bounds__(NW * 32) block_merge_kernel(const MergeParams 
     const int row_end = npos * G * (part + 1) / parts;
     for (int row = npos * G * part / parts + rb * NW + warp; row < row_end; row += CTAS * NW) {
       Merged<D> m;
-      m.add(0, parts, lane, p.tile_lse, p.tile_o, [&](int k) {
-        return (static_cast<int64_t>(first + k) * p.num_kv_heads + kvh) * ROWS + row;
-      });
+      auto at = [&](int k) { return (static_cast<int64_t>(first + k) * p.num_kv_heads + kvh) * ROWS + row; };
+      if (parts <= 2)
+        m.template add<2>(0, parts, lane, p.tile_lse, p.tile_o, at);
+      else
+        m.template add<8>(0, parts, lane, p.tile_lse, p.tile_o, at);
       m.template store<E>(p.out + static_cast<int64_t>(row0 + row / G) * p.num_heads * D +
                               static_cast<int64_t>(kvh * G + row % G) * D,
                           lane);
@@ -957,7 +959,7 @@ __global__ void __launch_bounds__(NW * 32) block_merge_kernel(const MergeParams 
     const int col = col0 + warp % wc;
     Merged<D> m;
     if (col < cols)
-      m.add(np * sub / subs, np * (sub + 1) / subs, lane, p.part_lse, p.part_o, [&](int k) {
+      m.template add<8>(np * sub / subs, np * (sub + 1) / subs, lane, p.part_lse, p.part_o, [&](int k) {
         const int item = min(max(k == np - 1 && rest >= 0 ? rest : full0 + k, 0), p.max_items - 1);
         return (static_cast<int64_t>(item) * p.num_kv_heads + kvh) * kCols + col;
       });

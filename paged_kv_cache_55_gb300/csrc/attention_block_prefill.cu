@@ -62,6 +62,16 @@ __device__ __forceinline__ float4 ld_scales(uint32_t addr) {
   return v;
 }
 
+// One thread of the converged warp, the same every time. With the operands
+// broadcast, the compiler keeps an MMA's descriptors in uniform registers
+// instead of moving each there from a thread's.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile("{\n .reg .pred q;\n .reg .b32 l;\n elect.sync l|q, 0xffffffff;\n selp.u32 %0, 1, 0, q;\n}\n" : "=r"(p));
+  return p != 0;
+}
+__device__ __forceinline__ uint32_t uniform(uint32_t v) { return __shfl_sync(0xffffffffu, v, 0); }
+
 // Row maximum of 32 scores under block scales (at shared address sc): s * (rowf * kf) + lv per group, as separately rounded operations. kf
 // and rowf are positive, so a group's largest raw score gives its largest
 // scaled one.
@@ -461,7 +471,8 @@ __global__ void __launch_bounds__(kTileThreads8, 1)
     // unit is read by the halves with r < nkt_h: the first of them waits for
     // the K/V loads, the last one's commit releases the buffers.
     constexpr uint32_t DHI = desc_hi(1024);
-    const uint32_t q_lo0 = desc_lo(sQ0, 16), q_lo1 = desc_lo(sQ0 + Lay::Q_BYTES, 16);
+    const uint32_t utmem = uniform(tmem);
+    const uint32_t q_lo0 = uniform(desc_lo(sQ0, 16)), q_lo1 = uniform(desc_lo(sQ0 + Lay::Q_BYTES, 16));
     const uint32_t k_lo = desc_lo(sRing, 16);  // slot 0
     // V (MN-major): LBO = distance between the two 64-element atoms along d,
     // SBO = distance between 8-key groups along K; K step ks at byte 2048 ks
@@ -481,10 +492,10 @@ __global__ void __launch_bounds__(kTileThreads8, 1)
       auto slot_of = [&](int kt, int v) { return (ring0 + 2 * kt + v) % SLOTS; };
       auto full_parity = [&](int kt, int v) { return ((ring0 + 2 * kt + v) / SLOTS) & 1u; };
       auto mma_s = [&](int kt, int h) {
-        if (lane == 0) {
+        const uint32_t klo = uniform(k_lo + slot_of(kt, 0) * SLOT_STEP), qlo = h ? q_lo1 : q_lo0;
+        const uint32_t d = utmem + h * Tm::HALF + Tm::SP;
+        if (elect_one()) {
           tc_fence_after();
-          const uint32_t klo = k_lo + slot_of(kt, 0) * SLOT_STEP, qlo = h ? q_lo1 : q_lo0;
-          const uint32_t d = tmem + h * Tm::HALF + Tm::SP;
           mma_ss<0>(d, qlo, DHI, klo, DHI, IDESC_S);
 #pragma unroll
           for (int ks = 1; ks < KSTEPS_S; ++ks) {
@@ -535,10 +546,10 @@ __global__ void __launch_bounds__(kTileThreads8, 1)
             }
             __syncwarp();
           }
-          if (lane == 0) {
+          const uint32_t vlo = uniform(v_lo + vslot * SLOT_STEP);
+          const uint32_t t = utmem + h * Tm::HALF;
+          if (elect_one()) {
             tc_fence_after();
-            const uint32_t vlo = v_lo + vslot * SLOT_STEP;
-            const uint32_t t = tmem + h * Tm::HALF;
             // one fp16 P per key: K step ks at column 8 ks (+ 32 for the second part's keys)
             auto pcol = [](int ks) { return 8 * ks + (ks >= 4 ? 32 : 0); };
             if (kt == 0)
@@ -853,7 +864,7 @@ __global__ void __launch_bounds__(kTileThreads8, 1)
   // for work still in flight: the MMA thread's products (one last commit)
   // and the producer's loads (loads into a buffer complete in order, so
   // waiting for the last SLOTS issued suffices).
-  if (warp == kMmaWarp && lane == 0) {
+  if (warp == kMmaWarp && elect_one()) {  // the thread that issued them
     tc_commit(bar(Lay::B_DRAIN));
     if (!mbar_wait_bounded(bar(Lay::B_DRAIN), 0, kTcWaitTimeoutNs)) failed = true;
   }
