@@ -179,15 +179,17 @@ size_t pa_attention_workspace_size(int32_t num_seqs, int32_t total_q_tokens, int
                                    int32_t head_dim, int32_t block_size) {
   if (max_query_len < 0 || max_seq_len < max_query_len) return 0;
   if (!supported_dims(num_heads, num_kv_heads, head_dim, block_size)) return 0;
-  // one size for every cache type: the largest of the plans
+  // one size for every cache type: the largest of the plans (bounds that the
+  // one with block scales cannot hold are refused by that call alone)
   pa::WorkspaceLayout w16, w8;
   pa::BlockWorkspace wb;
   if (!pa::workspace_layout(num_seqs, total_q_tokens, max_seq_len, num_heads, num_kv_heads, head_dim, false, w16) ||
-      !pa::workspace_layout(num_seqs, total_q_tokens, max_seq_len, num_heads, num_kv_heads, head_dim, true, w8) ||
-      !pa::block_workspace_layout(num_seqs, total_q_tokens, max_query_len, max_seq_len, num_heads, num_kv_heads,
-                                  head_dim, wb))
+      !pa::workspace_layout(num_seqs, total_q_tokens, max_seq_len, num_heads, num_kv_heads, head_dim, true, w8))
     return 0;
   const size_t w = w16.total > w8.total ? w16.total : w8.total;
+  if (!pa::block_workspace_layout(num_seqs, total_q_tokens, max_query_len, max_seq_len, num_heads, num_kv_heads,
+                                  head_dim, wb))
+    return w;
   return w > wb.total ? w : wb.total;
 }
 

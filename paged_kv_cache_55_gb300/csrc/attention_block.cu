@@ -30,9 +30,9 @@
 //   * block-table entries are loaded one tile ahead, the boxes of a tile are
 //     issued by as many lanes, and its scales travel with it by cp.async on
 //     the same mbarrier.
-// Measured (256 requests, 32 / 8 heads of 128, 958 MB): 167 us under a
-// counter, 5.8 TB/s; the same kernel with the products taken out takes 153 us,
-// so what is left is the loads' own rate (2 KB boxes of 128-byte rows: 6.3
+// Measured (256 requests, 32 / 8 heads of 128, 958 MB): a step of 173 us; the
+// decode kernel 167 us under a counter, 5.8 TB/s, and with the products taken
+// out 153 us, so what is left is the loads' own rate (2 KB boxes of 128-byte rows: 6.3
 // TB/s) and the end of the step, where warps finish unevenly. Tried and not
 // kept: K as E4M3 products of a q split into E4M3 terms (no widening; 5 %
 // slower at 256 requests, the same at 8 x 32768), 16-byte cp.async in place of
@@ -1176,12 +1176,20 @@ bool block_workspace_layout(int32_t num_seqs, int32_t total_q, int32_t max_query
       num_heads % num_kv_heads != 0 || num_heads / num_kv_heads > kCols)
     return false;
   const int G = num_heads / num_kv_heads;
-  // a request of t key tiles gives at most t / U + 1 items, U >= total / (kUnitsPerWarp * warps), or
-  // U >= total / warps when pairs are few
+  // The most items that unit_tiles leaves (per KV head): one wave of units when
+  // pairs are few; else one item more per request than full units, which are
+  // those of one wave (units below kMinUnit), or else of kMinUnit tiles at least
+  // and kUnitsPerWarp waves at most. Never more than there are tiles.
   const int64_t key_tiles = (static_cast<int64_t>(max_seq_len) + kTile - 1) / kTile;
-  const int64_t full = (kUnitsPerWarp * unit_warps(head_dim) + num_kv_heads - 1) / num_kv_heads;
-  int64_t items = static_cast<int64_t>(num_seqs) * key_tiles;
-  if (items > num_seqs + full) items = num_seqs + full;
+  const int64_t all_tiles = static_cast<int64_t>(num_seqs) * key_tiles;
+  const int64_t warps = unit_warps(head_dim), wave = (warps + num_kv_heads - 1) / num_kv_heads;
+  int64_t items = wave;
+  if (static_cast<int64_t>(num_seqs) * num_kv_heads * 8 > warps) {
+    int64_t full = (kUnitsPerWarp * warps + num_kv_heads - 1) / num_kv_heads;
+    if (full > all_tiles / kMinUnit) full = all_tiles / kMinUnit;
+    items = num_seqs + (full > wave ? full : wave);
+  }
+  if (items > all_tiles) items = all_tiles;
   const int rows = prefill_tile_rows(head_dim);
   const int64_t tiles = (static_cast<int64_t>(total_q) * G + rows - 1) / rows + num_seqs;
   if (items * num_kv_heads > (1LL << 30) || tiles * num_kv_heads > (1LL << 30) ||

@@ -12,11 +12,23 @@
 //     takes P'_j / vs_j, the plain weight. The producer stages a range's
 //     scales (K factor, log2 and inverse of V's) per group of GRP keys that
 //     share a block: 16, or 8 for 8-token blocks. A group costs a few
-//     operations, a key none; measured on 16 chunks of 512 (188 GFLOP): the
-//     tiles take 0.33 ms, against 0.31 over one scale per cache;
+//     operations, a key none;
 //   * parts. The planner splits tiles over their keys when there are too few
 //     to fill the SMs; a part writes its rows' normalised fp32 outputs and
 //     log2-sum-exps to a slot, and the merge kernel joins them.
+// Bound by the chain of a half: the tensor core takes 1000 cycles for P V of a
+// range and S of the next, the softmax about 4000 (two TMEM reads, the maxima's
+// exchange, 64 exponents a thread), and P lies over S, so neither runs under
+// the other of its own half; with two halves the tensor core is a third busy.
+// Measured (a step of 16 chunks of 512 and 48 decode requests over 8-bit
+// caches, 188 GFLOP): 263 us. What brought it there, in turn: Q loaded along
+// rows and not a lane per row (325 -> 280), q sent towards L2 by the producer
+// (275), MMAs issued by an elected thread with broadcast descriptors (263).
+// Tried and not kept: P handed over in two halves (2 % slower: the issuing
+// thread then waits inside a product while the other half is ready), the next
+// tile's record read before the last range (3 % slower, registers), ring
+// slots counted instead of divided and one arrival per warp at the exchange
+// (no difference).
 #include <type_traits>
 
 #include "attention_tile.cuh"
@@ -72,9 +84,9 @@ __device__ __forceinline__ bool elect_one() {
 }
 __device__ __forceinline__ uint32_t uniform(uint32_t v) { return __shfl_sync(0xffffffffu, v, 0); }
 
-// Row maximum of 32 scores under block scales (at shared address sc): s * (rowf * kf) + lv per group, as separately rounded operations. kf
-// and rowf are positive, so a group's largest raw score gives its largest
-// scaled one.
+// Row maximum of 32 scores under block scales (at shared address sc): s *
+// (rowf * kf) + lv per group, as separately rounded operations. kf and rowf are
+// positive, so a group's largest raw score gives its largest scaled one.
 template <int GRP>
 __device__ __forceinline__ float scaled_max32(const uint32_t (&s)[32], int ck0, int lim, float rowf, uint32_t sc) {
   float m = -INFINITY;

@@ -22,6 +22,12 @@
 // it loaded, after every load of its rows, so q_out may be q and key_out may be
 // key. A unit of work is BATCH such row groups of one token, all their loads
 // issued first; the weights wait in shared memory as floats.
+//
+// Bound by HBM when there are many tokens, by launch and load latency in a
+// decode step. Measured (32 / 8 heads of 128, bf16): 8432 tokens 39.8 us, 5.3
+// TB/s, against 49.5 with one row group at a time and weights converted per
+// row; what is left is issue (0.48 per cycle at 24 % of the warps: the 123
+// registers that hold four groups). 256 tokens 3.6 us, one token 2.4.
 #include "cache_write.cuh"
 #include "pa_common.cuh"
 #include "pa_launch.h"
