@@ -395,7 +395,9 @@ pa_status pa_reshape_and_cache_fp8_block(const void *key, const void *value, int
  *   out[t][h][:] = round( sum_j softmax_j(scale * q[t][h] . (ks_j * Kc[j]))
  *                         * (vs_j * Vc[j]) ),  ks_j, vs_j of key j's block.
  * Block scales that are read must be positive and finite. scale must be
- * positive (PA_ERR_DIMS otherwise).
+ * positive (PA_ERR_DIMS otherwise). A NaN value code of a key gives NaN in its
+ * column of the rows that see the key, and may in rows of the same request's
+ * chunk that come before it; it reaches no other request or KV head.
  */
 pa_status pa_attention_varlen_fp8_block(const void *q, int64_t q_token_stride,
                                         const void *key_cache, const void *value_cache,

@@ -183,6 +183,31 @@ def test_a_growing_scale_keeps_nan_codes_and_a_bad_scale_counts_as_zero():
     s.check_scatter()
 
 
+def test_appending_under_a_scale_that_is_no_power_of_two():
+    """A cache made elsewhere: its larger scale stays, new rows take E4M3(x / scale) of the fp32 quotient, old
+    rows keep their codes."""
+    s = Step([5, 20, 9], [3, 1, 60], 2, 2, 128, seed=28, spread=0.3)
+    firsts = [int(s.tables[0, 0]), int(s.tables[1, 1]), int(s.tables[2, 0])]
+    for p in firsts:
+        s.ks[p], s.vs[p] = np.float32([0.7, 1.1]), np.float32([0.9, 0.3])
+    s.upload()
+    kc, vc = s.kc.copy(), s.vc.copy()
+    s.scatter()
+    torch.cuda.synchronize()
+    for b, p in enumerate(firsts):
+        held = int(s.lens[b] - (s.starts[b + 1] - s.starts[b])) % 16
+        n = min(16 - held, int(s.starts[b + 1] - s.starts[b]))
+        t0 = int(s.starts[b])
+        for rows, codes, old, scales, d_scales in ((s.key, s.d_kc, kc, s.ks, s.d_ks),
+                                                   (s.value, s.d_vc, vc, s.vs, s.d_vs)):
+            got = codes[p].cpu().numpy()
+            assert np.array_equal(d_scales[p].cpu().numpy(), scales[p].astype(np.float32))
+            assert np.array_equal(got[:held], old[p, :held])
+            quotient = rows[t0:t0 + n].float().cpu().numpy() / scales[p].astype(np.float32)[None, :, None]
+            assert np.array_equal(got[held:held + n], R.encode(quotient.astype(np.float64)))
+    assert B.pa_debug_status() == 0
+
+
 def test_scatter_refuses_on_the_device_and_leaves_the_rest():
     s = Step([0, 20, 5, 9], [4, 4, 4, 4], 2, 2, 64, seed=9)
     s.tables[1, 1] = s.nb                # block id out of range
@@ -289,6 +314,40 @@ def test_queries_beyond_fp16(q_scale):
     s.scatter()
     s.attention()
     s.check_attention()
+
+
+@pytest.mark.parametrize("head_dim", [64, 80, 128, 256])
+def test_some_queries_beyond_fp16(head_dim):
+    """Only the rows that need it are scaled; their neighbours in the tile are not."""
+    s = Step([40, 900], [150, 1], 8, 2, head_dim, seed=29, spread=0.3)
+    s.q[::7, 3] *= 5.0e5
+    s.q[5, 1, 11] = 3.0e5
+    s.scatter()
+    s.attention()
+    s.check_attention()
+
+
+@pytest.mark.parametrize("head_dim", [64, 96, 128, 256])
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+def test_query_rows_at_any_even_stride_and_offset(dtype, head_dim):
+    """q 4-byte aligned only, its rows apart: the bits of contiguous rows."""
+    s = Step([40, 900, 3], [150, 1, 2], 8, 2, head_dim, dtype=dtype, seed=30, spread=0.3)
+    s.scatter()
+    s.attention()
+    torch.cuda.synchronize()
+    want = s.out.clone()
+    n = 8 * head_dim
+    for offset, stride in ((2, n + 2), (8, n + 8), (0, n + 4)):
+        buf = torch.full((s.T * stride + offset,), float("nan"), dtype=s.q.dtype, device="cuda")
+        rows = buf[offset:].view(s.T, stride)[:, :n].view(s.T, 8, head_dim)
+        rows.copy_(s.q)
+        contiguous, s.q = s.q, rows
+        s.out.fill_(float("nan"))
+        s.attention()
+        torch.cuda.synchronize()
+        assert torch.equal(s.out, want)
+        s.q = contiguous
+    assert B.pa_debug_status() == 0
 
 
 def test_any_positive_scale_is_read_exactly():
