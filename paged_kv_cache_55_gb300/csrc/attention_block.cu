@@ -99,9 +99,9 @@ __host__ __device__ inline int64_t unit_tiles(int64_t total, int64_t pairs, int6
 constexpr int kSplitSms = 152, kMinRanges = 2, kRangeKeys = 128;
 constexpr int kNoSplit = 1 << 30;
 __host__ __device__ inline int part_items(int num_kv_heads) { return kSplitSms / num_kv_heads; }
+__host__ __device__ inline int most_split_tiles(int num_kv_heads) { return part_items(num_kv_heads) * 3 / 4; }
 __device__ __forceinline__ int part_ranges(int64_t tiles, int64_t ranges, int num_kv_heads) {
   const int64_t slots = part_items(num_kv_heads);
-  if (tiles * 4 > slots * 3) return kNoSplit;
   const int64_t u = (ranges + slots - tiles - 1) / (slots - tiles);
   return static_cast<int>(u < kMinRanges ? kMinRanges : u);
 }
@@ -252,7 +252,7 @@ __global__ void __launch_bounds__(NT) block_plan_kernel(const PlanParams p) {
   griddep_launch_dependents();
   const bool once = p.num_seqs <= NT;
   const bool chunks = p.max_query_len > p.rows_per_item;
-  const int most_split = chunks && p.max_part_items > 0 ? part_items(p.num_kv_heads) * 3 / 4 : 0;  // tiles
+  const int most_split = chunks && p.max_part_items > 0 ? most_split_tiles(p.num_kv_heads) : 0;
   auto tile_ranges = [&](int len, int ql, int t) {  // 128-key ranges that tile t of a request walks
     return (len - ql + min((t + 1) * p.tile_pos, ql) - 1) / kRangeKeys + 1;
   };
@@ -1196,9 +1196,11 @@ bool block_workspace_layout(int32_t num_seqs, int32_t total_q, int32_t max_query
       static_cast<int64_t>(num_seqs) * num_kv_heads > (1LL << 30))
     return false;
   w.max_items = static_cast<int32_t>(items > 0 ? items : 1);
-  // parts of split prefill tiles: at least kMinRanges ranges each
+  // parts of split prefill tiles: at least kMinRanges ranges each; none where the
+  // rows that no decode request can hold already make more tiles than are split
   int64_t split_items = 0;
-  if (max_query_len > kCols / G) {
+  const int64_t chunk_rows = total_q - static_cast<int64_t>(num_seqs) * (kCols / G);
+  if (max_query_len > kCols / G && chunk_rows * G <= static_cast<int64_t>(most_split_tiles(num_kv_heads)) * rows) {
     const int64_t most = (static_cast<int64_t>(max_seq_len) + kMinRanges * kRangeKeys - 1) / (kMinRanges * kRangeKeys);
     split_items = part_items(num_kv_heads);
     if (most <= 1) split_items = 0;
