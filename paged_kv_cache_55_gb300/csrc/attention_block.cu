@@ -30,8 +30,8 @@
 //   * block-table entries are loaded one tile ahead, the boxes of a tile are
 //     issued by as many lanes, and its scales travel with it by cp.async on
 //     the same mbarrier.
-// Measured (256 requests, 32 / 8 heads of 128, 958 MB): a step of 173 us; the
-// decode kernel 167 us under a counter, 5.8 TB/s, and with the products taken
+// Measured (256 requests, 32 / 8 heads of 128, 958 MB): a step of 173 to 178
+// us; the decode kernel 163 to 167 us under a counter, 5.8 TB/s, and with the products taken
 // out 153 us, so what is left is the loads' own rate (2 KB boxes of 128-byte rows: 6.3
 // TB/s) and the end of the step, where warps finish unevenly. Tried and not
 // kept: K as E4M3 products of a q split into E4M3 terms (no widening; 5 %
