@@ -120,28 +120,28 @@ __device__ __forceinline__ float scaled_max32(const uint32_t (&s)[32], int ck0, 
 // k0 + i visible while k0 + i < lim), one fp16 value per key, summed into *sum and
 // stored at TMEM column `col` of this thread's lane (8 columns):
 // P' = 2^(s * kf + lv - ms) carries the V scale 2^lv, so O accumulates P' times
-// codes; the row sum takes P' / 2^lv. EXACT rows also apply the row's factor
-// (1 otherwise).
-template <int GRP, bool EXACT>
+// codes; the row sum takes P' / 2^lv. RARE: the row's factor (1 otherwise),
+// every operation rounded by itself, and the mask; without it all 16 keys are
+// visible (or the row is none of the tile's and is never stored).
+template <int GRP, bool RARE>
 __device__ __forceinline__ void probs16_scaled_store(const uint32_t *s, int k0, int lim, float rowf, float ms,
                                                      float &sum, uint32_t col, const float4 &c) {
-  const bool full = k0 + 16 <= lim;
   uint32_t hv[8];
 #pragma unroll
   for (int g = 0; g < 16 / GRP; ++g) {
     const float kf = g == 0 ? c.x : c.z, lv = g == 0 ? c.y : c.w;
-    const float f = EXACT ? __fmul_rn(rowf, kf) : kf, add = lv - ms;
+    const float f = RARE ? __fmul_rn(rowf, kf) : kf, add = lv - ms;
     float acc0 = 0.f, acc1 = 0.f;
 #pragma unroll
     for (int j = 0; j < GRP / 2; ++j) {
       const int i = GRP / 2 * g + j;
       float x0 = __uint_as_float(s[2 * i]), x1 = __uint_as_float(s[2 * i + 1]);
-      if (!full) {
+      if (RARE) {
         x0 = k0 + 2 * i < lim ? x0 : -INFINITY;
         x1 = k0 + 2 * i + 1 < lim ? x1 : -INFINITY;
       }
       float e0, e1;
-      if (EXACT) {
+      if (RARE) {
         e0 = __fsub_rn(__fadd_rn(__fmul_rn(x0, f), lv), ms);
         e1 = __fsub_rn(__fadd_rn(__fmul_rn(x1, f), lv), ms);
       } else {
@@ -761,7 +761,8 @@ __global__ void __launch_bounds__(kTileThreads8, 1)
         }
         const float ms = m_used == -INFINITY ? 0.f : m_used;
         float sum = 0.f;
-        const bool exact = __any_sync(FULL, fabsf(ms) > 4096.f || rowf != 1.f);
+        const bool rare =
+            __any_sync(FULL, fabsf(ms) > 4096.f || rowf != 1.f || (row_valid && ck0 + PART_KEYS > lim));
         // P over the scores it came from, one UMMA K step (16 keys) at a
         // time, the scores read again from TMEM: a loop unrolled twice, not
         // four times (the hot code of twenty warps shares the instruction
@@ -770,7 +771,7 @@ __global__ void __launch_bounds__(kTileThreads8, 1)
         // P of step ks (8 columns at 8 ks) covers only scores read by
         // earlier steps. Rare cases stay out of the loop (inside it, as a
         // branch per step, they cost 2 %).
-        if (exact) {
+        if (rare) {
 #pragma unroll 1
           for (int ks = 0; ks < PART_KEYS / 16; ++ks) {
             const float4 c = ld_scales(sc + 16 * ks);
@@ -1404,13 +1405,14 @@ __global__ void __launch_bounds__(kWideThreads, 1)
         }
         const float ms = m_used == -INFINITY ? 0.f : m_used;
         float sum = 0.f;
-        const bool exact = __any_sync(FULL, fabsf(ms) > 4096.f || rowf != 1.f);
+        const bool rare =
+            __any_sync(FULL, fabsf(ms) > 4096.f || rowf != 1.f || (row_valid && ck0 + 64 > lim));
 #pragma unroll 1
         for (int ks = 0; ks < 4; ++ks) {
           const float4 c = ld_scales(sc + 16 * ks);
           uint32_t t[16];
           tmem_ld16_wait(sp + 16 * ks, t);
-          if (exact)
+          if (rare)
             probs16_scaled_store<GRP, true>(t, ck0 + 16 * ks, lim, rowf, ms, sum, sp + 8 * ks, c);
           else
             probs16_scaled_store<GRP, false>(t, ck0 + 16 * ks, lim, rowf, ms, sum, sp + 8 * ks, c);
