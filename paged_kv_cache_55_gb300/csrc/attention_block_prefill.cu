@@ -87,7 +87,7 @@ __device__ __forceinline__ uint32_t uniform(uint32_t v) { return __shfl_sync(0xf
 // Row maximum of 32 scores under block scales (at shared address sc): s *
 // (rowf * kf) + lv per group, as separately rounded operations. kf and rowf are
 // positive, so a group's largest raw score gives its largest scaled one.
-template <int GRP>
+template <int GRP, bool MASK>
 __device__ __forceinline__ float scaled_max32(const uint32_t (&s)[32], int ck0, int lim, float rowf, uint32_t sc) {
   float m = -INFINITY;
   float4 v;
@@ -97,7 +97,7 @@ __device__ __forceinline__ float scaled_max32(const uint32_t (&s)[32], int ck0, 
     if (g % PER16 == 0) v = ld_scales(sc + 16 * (g / PER16));
     const float kf = g % PER16 == 0 ? v.x : v.z, lv = g % PER16 == 0 ? v.y : v.w;
     float t;
-    if (ck0 + 32 <= lim) {
+    if (!MASK || ck0 + 32 <= lim) {
       t = max3(__uint_as_float(s[GRP * g]), __uint_as_float(s[GRP * g + 1]), __uint_as_float(s[GRP * g + 2]));
       float u = max3(__uint_as_float(s[GRP * g + 3]), __uint_as_float(s[GRP * g + 4]), __uint_as_float(s[GRP * g + 5]));
 #pragma unroll
@@ -748,8 +748,14 @@ __global__ void __launch_bounds__(kTileThreads8, 1)
         // fused multiply-add): the exponents below are bounded by exactly this
         // difference. The other warp reads its scores before either writes P.
         float mx;
-        mx = scaled_max32<GRP>(s0, ck0, lim, rowf, sc);
-        mx = fmaxf(mx, scaled_max32<GRP>(s1, ck0 + 32, lim, rowf, sc + 32));
+        // (64 keys a warp and range; a row that is none of the tile's is not stored, and needs no mask)
+        const bool masked = __any_sync(FULL, row_valid && ck0 + 64 > lim);
+        if (masked)
+          mx = fmaxf(scaled_max32<GRP, true>(s0, ck0, lim, rowf, sc),
+                     scaled_max32<GRP, true>(s1, ck0 + 32, lim, rowf, sc + 32));
+        else
+          mx = fmaxf(scaled_max32<GRP, false>(s0, ck0, lim, rowf, sc),
+                     scaled_max32<GRP, false>(s1, ck0 + 32, lim, rowf, sc + 32));
         const float mo = exchange(mx);
         if (failed) break;
         const float cm = fmaxf(mx, mo);
@@ -761,8 +767,7 @@ __global__ void __launch_bounds__(kTileThreads8, 1)
         }
         const float ms = m_used == -INFINITY ? 0.f : m_used;
         float sum = 0.f;
-        const bool rare =
-            __any_sync(FULL, fabsf(ms) > 4096.f || rowf != 1.f || (row_valid && ck0 + PART_KEYS > lim));
+        const bool rare = masked || __any_sync(FULL, fabsf(ms) > 4096.f || rowf != 1.f);
         // P over the scores it came from, one UMMA K step (16 keys) at a
         // time, the scores read again from TMEM: a loop unrolled twice, not
         // four times (the hot code of twenty warps shares the instruction
@@ -1392,8 +1397,14 @@ __global__ void __launch_bounds__(kWideThreads, 1)
         wait_warp(sc_bar(fi), (gr / Lay::SCALE_SLOTS) & 1u, failed);
         if (failed) break;
         sc = base + Lay::SC_OFF + fi * kScaleSlotBytes + part * 64;
-        mx = scaled_max32<GRP>(s0, ck0, lim, rowf, sc);
-        mx = fmaxf(mx, scaled_max32<GRP>(s1, ck0 + 32, lim, rowf, sc + 32));
+        // (64 keys a warp and range; a row that is none of the tile's is not stored, and needs no mask)
+        const bool masked = __any_sync(FULL, row_valid && ck0 + 64 > lim);
+        if (masked)
+          mx = fmaxf(scaled_max32<GRP, true>(s0, ck0, lim, rowf, sc),
+                     scaled_max32<GRP, true>(s1, ck0 + 32, lim, rowf, sc + 32));
+        else
+          mx = fmaxf(scaled_max32<GRP, false>(s0, ck0, lim, rowf, sc),
+                     scaled_max32<GRP, false>(s1, ck0 + 32, lim, rowf, sc + 32));
         const float mo = exchange(mx);
         if (failed) break;
         const float cm = fmaxf(mx, mo);
@@ -1405,8 +1416,7 @@ __global__ void __launch_bounds__(kWideThreads, 1)
         }
         const float ms = m_used == -INFINITY ? 0.f : m_used;
         float sum = 0.f;
-        const bool rare =
-            __any_sync(FULL, fabsf(ms) > 4096.f || rowf != 1.f || (row_valid && ck0 + 64 > lim));
+        const bool rare = masked || __any_sync(FULL, fabsf(ms) > 4096.f || rowf != 1.f);
 #pragma unroll 1
         for (int ks = 0; ks < 4; ++ks) {
           const float4 c = ld_scales(sc + 16 * ks);
