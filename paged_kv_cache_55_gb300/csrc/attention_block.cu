@@ -31,10 +31,10 @@
 //     issued by as many lanes, and its scales travel with it by cp.async on
 //     the same mbarrier.
 // Measured (256 requests, 32 / 8 heads of 128, 958 MB): a step of 173 to 178
-// us; the decode kernel 163 to 167 us under a counter, 5.8 TB/s, and with the products taken
-// out 153 us, so what is left is the loads' own rate (2 KB boxes of 128-byte rows: 6.3
-// TB/s) and the end of the step, where warps finish unevenly. Tried and not
-// kept: K as E4M3 products of a q split into E4M3 terms (no widening; 5 %
+// us; the decode kernel 163 to 167 us under a counter, 5.8 TB/s, and with the
+// products taken out 153 us, so what is left is the loads' own rate (2 KB boxes
+// of 128-byte rows: 6.3 TB/s) and the end of the step, where warps finish
+// unevenly. Tried and not kept: K as E4M3 products of a q split into E4M3 terms (no widening; 5 %
 // slower at 256 requests, the same at 8 x 32768), 16-byte cp.async in place of
 // TMA (2-4 % slower), units that shrink towards the end of the queue (17 %
 // slower: a unit's start and its partial cost more than the tail), 8, 10 and
@@ -909,9 +909,11 @@ struct Merged {
 };
 
 // CTAs of NW warps that merge a part's share (half at most) of a split prefill
-// tile's rows, a warp per row
+// tile's rows, up to four rows a warp, so that the parts of 152 SMs fit about
+// one wave (7 chunks of 131 over 1500 keys: the step 34.7 us, with two rows a
+// warp 35.2, with one 37.5)
 template <int D, int NW>
-constexpr int kTileMergeCtas = prefill_tile_rows(D) / 2 / NW;
+constexpr int kTileMergeCtas = prefill_tile_rows(D) / 8 / NW;
 
 template <int D, int G, typename E, int NW>
 __global__ void __launch_bounds__(NW * 32) block_merge_kernel(const MergeParams p) {

@@ -17,18 +17,20 @@
 //     to fill the SMs; a part writes its rows' normalised fp32 outputs and
 //     log2-sum-exps to a slot, and the merge kernel joins them.
 // Bound by the chain of a half: the tensor core takes 1000 cycles for P V of a
-// range and S of the next, the softmax about 4000 (two TMEM reads, the maxima's
-// exchange, 64 exponents a thread), and P lies over S, so neither runs under
-// the other of its own half; with two halves the tensor core is a third busy.
+// range and S of the next, the softmax 3000 to 4000 (two TMEM reads, the
+// maxima's exchange, 64 exponents a thread), and P lies over S, so neither runs
+// under the other of its own half; with two halves the tensor core is 41 % busy.
 // Measured (a step of 16 chunks of 512 and 48 decode requests over 8-bit
-// caches, 188 GFLOP): 263 us. What brought it there, in turn: Q loaded along
-// rows and not a lane per row (325 -> 280), q sent towards L2 by the producer
-// (275), MMAs issued by an elected thread with broadcast descriptors (263).
+// caches, 188 GFLOP): 241 us, of which the tiles 214 under a counter. What
+// brought it there, in turn: Q loaded along rows and not a lane per row (325 ->
+// 280), q sent towards L2 by the producer (275), MMAs issued by an elected
+// thread with broadcast descriptors (263), no masks where all keys are visible
+// (241).
 // Tried and not kept: P handed over in two halves (2 % slower: the issuing
 // thread then waits inside a product while the other half is ready), the next
 // tile's record read before the last range (3 % slower, registers), ring
-// slots counted instead of divided and one arrival per warp at the exchange
-// (no difference).
+// slots counted instead of divided, one arrival per warp at the exchange, and
+// the loop over P unrolled in full (no difference).
 #include <type_traits>
 
 #include "attention_tile.cuh"
