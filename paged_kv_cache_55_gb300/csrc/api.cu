@@ -213,7 +213,8 @@ pa_status attention_call(const void *q, int64_t q_token_stride, const void *key_
                          const int32_t *query_start_loc, int32_t num_seqs, int32_t total_q_tokens,
                          int32_t max_query_len, int32_t max_seq_len, int32_t num_heads, int32_t num_kv_heads,
                          int32_t head_dim, int32_t block_size, int64_t num_blocks, float scale, bool kv_fp8,
-                         float k_scale, float v_scale, const float *k_scales, const float *v_scales, void *out, void *workspace, size_t workspace_bytes,
+                         float k_scale, float v_scale, const float *k_scales, const float *v_scales, void *out,
+                         void *workspace, size_t workspace_bytes,
                          int32_t dtype, void *stream) {
   cudaEvent_t ev_start = t_ev_start, ev_stop = t_ev_stop, tile_start = t_tile_start, tile_stop = t_tile_stop;
   t_ev_start = t_ev_stop = t_tile_start = t_tile_stop = nullptr;
