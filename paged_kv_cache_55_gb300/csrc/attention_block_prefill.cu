@@ -195,6 +195,88 @@ __device__ __forceinline__ void st_scales(uint32_t slot, int group, float kf, fl
     asm volatile("st.shared.v2.f32 [%0], {%1, %2};\n" ::"r"(slot + 8 * group), "f"(kf), "f"(lv) : "memory");
 }
 
+// Sixteen rows of a unit's Q, row0 .. row0 + 15 of the tile (or half) whose
+// first position is `pos_base` of the unit (row r = (position, head), K-major),
+// to shared memory as fp16 or as they are, chunk c of a row at at(row, c).
+// Consecutive lanes take consecutive 16-byte chunks. Returns (lanes 0..15) the
+// softmax factor of row row0 + lane: 2^e, e > 0 for a scaled bf16 row. Measured
+// (16 chunks of 512, 6.7 tiles a CTA): a lane per row instead, 32 lines an
+// instruction, cost 36000 cycles between two tiles; at head_dim 256 (8 chunks of
+// 600, 16 / 4 heads) the step took 223 us against 199.
+template <int D, int G, typename E, typename At>
+__device__ __forceinline__ float load_q_rows(const BlockTileParams &p, const TileUnit &u, int pos_base, int row0,
+                                             int lane, At at) {
+  constexpr bool kBf16 = std::is_same<E, ElemBf16>::value;
+  constexpr int CPR = D / 8, NL = 16 * CPR / 32;  // chunks per row, and per lane
+  auto valid = [&](int row) { return pos_base + row / G < u.npos; };
+  auto q_row = [&](int row) {
+    return p.q + static_cast<int64_t>(u.row0 + pos_base + row / G) * p.q_stride +
+           static_cast<int64_t>(u.kvh * G + row % G) * D;
+  };
+  auto put = [&](int row, int c, uint4 w, float qmul) {
+    if constexpr (kBf16) {
+      w = make_uint4(ElemFp16::pack(ElemBf16::lo(w.x) * qmul, ElemBf16::hi(w.x) * qmul),
+                     ElemFp16::pack(ElemBf16::lo(w.y) * qmul, ElemBf16::hi(w.y) * qmul),
+                     ElemFp16::pack(ElemBf16::lo(w.z) * qmul, ElemBf16::hi(w.z) * qmul),
+                     ElemFp16::pack(ElemBf16::lo(w.w) * qmul, ElemBf16::hi(w.w) * qmul));
+    }
+    asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};\n" ::"r"(at(row, c)), "r"(w.x), "r"(w.y), "r"(w.z),
+                 "r"(w.w)
+                 : "memory");
+  };
+  // q is only required to be 4-byte aligned: 16-byte loads when rows allow them
+  const bool q16 = (reinterpret_cast<uintptr_t>(p.q) & 15u) == 0 && (p.q_stride & 7) == 0;
+  uint4 w[NL];
+#pragma unroll
+  for (int i = 0; i < NL; ++i) {
+    const int row = row0 + (32 * i + lane) / CPR, c = (32 * i + lane) % CPR;
+    w[i] = make_uint4(0u, 0u, 0u, 0u);
+    if (q16 && valid(row)) w[i] = __ldg(reinterpret_cast<const uint4 *>(q_row(row)) + c);
+  }
+  bool rare = !q16;  // or an element of magnitude 2^15 or more (or NaN) that fp16 may not hold
+  if constexpr (kBf16) {
+    uint32_t m = 0;
+#pragma unroll
+    for (int i = 0; i < NL; ++i) {
+      m = __vimax3_u16x2(m, w[i].x & 0x7FFF7FFFu, w[i].y & 0x7FFF7FFFu);
+      m = __vimax3_u16x2(m, w[i].z & 0x7FFF7FFFu, w[i].w & 0x7FFF7FFFu);
+    }
+    rare = rare || __any_sync(0xffffffffu, max(m & 0xffffu, m >> 16) >= 0x4700u);  // bf16 2^15
+  }
+  float rowf = 1.f;
+  if (!rare) {
+#pragma unroll
+    for (int i = 0; i < NL; ++i) put(row0 + (32 * i + lane) / CPR, (32 * i + lane) % CPR, w[i], 1.f);
+  } else if (lane < 16) {  // a lane per row
+    const int row = row0 + lane;
+    auto ldq = [&](int c) {
+      if (!valid(row)) return make_uint4(0u, 0u, 0u, 0u);
+      const uint32_t *q32 = reinterpret_cast<const uint32_t *>(q_row(row)) + 4 * c;
+      return make_uint4(__ldg(q32), __ldg(q32 + 1), __ldg(q32 + 2), __ldg(q32 + 3));
+    };
+    float qmul = 1.f;
+    if constexpr (kBf16) {
+      // 2^-e, e > 0 only when the row's largest |q| reaches 2^15
+      float amax = 0.f;
+#pragma unroll 1
+      for (int c = 0; c < CPR; ++c) {
+        const uint4 x = ldq(c);
+        const uint32_t v[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+          amax = fmaxf(amax, fmaxf(fabsf(ElemBf16::lo(v[k])), fabsf(ElemBf16::hi(v[k]))));
+      }
+      const int ex = static_cast<int>((__float_as_uint(amax) >> 23) & 0xffu) - 127;  // floor(log2(amax))
+      const int e = ex >= 15 ? min(ex - 14, 120) : 0;
+      qmul = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
+      rowf = __uint_as_float(static_cast<uint32_t>(127 + e) << 23);
+    }
+#pragma unroll 1
+    for (int c = 0; c < CPR; ++c) put(row, c, ldq(c), qmul);
+  }
+  return rowf;
+}
+
 template <int D, int G, typename E, int GRP>
 // Twenty warps, one CTA per SM.
 __global__ void __launch_bounds__(kTileThreads8, 1)
@@ -628,94 +710,15 @@ __global__ void __launch_bounds__(kTileThreads8, 1)
     uint32_t phh = 0;  // ranges this half has run so far
     uint32_t gvs = 0;  // ranges of the CTA's earlier units (both halves)
 
-    auto q_row = [&](const TileUnit &u, int row) {
-      return p.q + static_cast<int64_t>(u.row0 + h * POS_PER_HALF + row / G) * p.q_stride +
-             static_cast<int64_t>(u.kvh * G + row % G) * D;
-    };
-    // Q of the half for unit `u`: this warp stores 16 of its 32
-    // rows (row r = (position, head), K-major, swizzled), consecutive lanes
-    // consecutive 16-byte chunks, and returns (lanes 0..15) the softmax factor of row 16 part + lane: 2^e,
-    // e > 0 for a scaled bf16 row. Measured
-    // (16 chunks of 512, 6.7 tiles a CTA): a lane per row instead, 32 lines an
-    // instruction, cost 36000 cycles between two tiles.
+    // Q of the half for unit `u`: this warp's 16 rows; returns their factors (lanes 0..15)
     auto load_q = [&](const TileUnit &u) -> float {
       const uint32_t sQ = sQ0 + h * Lay::Q_BYTES;
-      const int row_w = quad * 32 + part * 16;  // this warp's first row
-      // q is only required to be 4-byte aligned: 16-byte loads when rows allow them
-      const bool q16 = (reinterpret_cast<uintptr_t>(p.q) & 15u) == 0 && (p.q_stride & 7) == 0;
-      auto ldq = [&](int row, int c) {
-        uint4 w = make_uint4(0u, 0u, 0u, 0u);
-        if (h * POS_PER_HALF + row / G < u.npos) {
-          const bf16 *qrow = q_row(u, row);
-          if (q16) {
-            w = __ldg(reinterpret_cast<const uint4 *>(qrow) + c);
-          } else {
-            const uint32_t *q32 = reinterpret_cast<const uint32_t *>(qrow) + 4 * c;
-            w = make_uint4(__ldg(q32), __ldg(q32 + 1), __ldg(q32 + 2), __ldg(q32 + 3));
-          }
-        }
-        return w;
-      };
-      auto stq = [&](int row, int c, uint4 w, float qmul) {
-        if constexpr (std::is_same<E, ElemBf16>::value) {
-          w = make_uint4(ElemFp16::pack(ElemBf16::lo(w.x) * qmul, ElemBf16::hi(w.x) * qmul),
-                         ElemFp16::pack(ElemBf16::lo(w.y) * qmul, ElemBf16::hi(w.y) * qmul),
-                         ElemFp16::pack(ElemBf16::lo(w.z) * qmul, ElemBf16::hi(w.z) * qmul),
-                         ElemFp16::pack(ElemBf16::lo(w.w) * qmul, ElemBf16::hi(w.w) * qmul));
-        }
-        asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};\n" ::"r"(sQ + Lay::off(row, c, Lay::Q_ATOM)), "r"(w.x),
-                     "r"(w.y), "r"(w.z), "r"(w.w)
-                     : "memory");
-      };
-      constexpr int CPR = D / 8, NL = 16 * CPR / 32;  // chunks per row, and per lane
-      uint4 w[NL];
-#pragma unroll
-      for (int i = 0; i < NL; ++i) {
-        const int row = row_w + (32 * i + lane) / CPR, c = (32 * i + lane) % CPR;
-        w[i] = make_uint4(0u, 0u, 0u, 0u);
-        if (q16 && h * POS_PER_HALF + row / G < u.npos)
-          w[i] = __ldg(reinterpret_cast<const uint4 *>(q_row(u, row)) + c);
-      }
-      bool rare = !q16;  // or an element of magnitude 2^15 or more (or NaN) that fp16 may not hold
-      float rowf = 1.f;
-      if constexpr (std::is_same<E, ElemBf16>::value) {
-        uint32_t m = 0;
-#pragma unroll
-        for (int i = 0; i < NL; ++i) {
-          m = __vimax3_u16x2(m, w[i].x & 0x7FFF7FFFu, w[i].y & 0x7FFF7FFFu);
-          m = __vimax3_u16x2(m, w[i].z & 0x7FFF7FFFu, w[i].w & 0x7FFF7FFFu);
-        }
-        rare = rare || __any_sync(FULL, max(m & 0xffffu, m >> 16) >= 0x4700u);  // bf16 2^15
-      }
-      if (!rare) {
-#pragma unroll
-        for (int i = 0; i < NL; ++i) stq(row_w + (32 * i + lane) / CPR, (32 * i + lane) % CPR, w[i], 1.f);
-      } else if (lane < 16) {  // a lane per row
-        const int row = row_w + lane;
-        float qmul = 1.f;
-        if constexpr (std::is_same<E, ElemBf16>::value) {
-          // 2^-e, e > 0 only when the row's largest |q| reaches 2^15
-          float amax = 0.f;
-#pragma unroll 1
-          for (int c = 0; c < CPR; ++c) {
-            const uint4 x = ldq(row, c);
-            const uint32_t v[4] = {x.x, x.y, x.z, x.w};
-#pragma unroll
-            for (int k = 0; k < 4; ++k)
-              amax = fmaxf(amax, fmaxf(fabsf(ElemBf16::lo(v[k])), fabsf(ElemBf16::hi(v[k]))));
-          }
-          const int ex = static_cast<int>((__float_as_uint(amax) >> 23) & 0xffu) - 127;  // floor(log2(amax))
-          const int e = ex >= 15 ? min(ex - 14, 120) : 0;
-          qmul = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
-          rowf = __uint_as_float(static_cast<uint32_t>(127 + e) << 23);
-        }
-#pragma unroll 1
-        for (int c = 0; c < CPR; ++c) stq(row, c, ldq(row, c), qmul);
-      }
+      const float mine = load_q_rows<D, G, E>(p, u, h * POS_PER_HALF, quad * 32 + part * 16, lane,
+                                              [&](int row, int c) { return sQ + Lay::off(row, c, Lay::Q_ATOM); });
       fence_proxy_async_smem();  // the MMA reads Q through the async proxy
       __syncwarp();
       if (lane == 0) mbar_arrive(bar(Lay::B_QF + h));
-      return rowf;
+      return mine;
     };
 
     TileUnit cur;
@@ -1320,65 +1323,27 @@ __global__ void __launch_bounds__(kWideThreads, 1)
     };
     const int g = r % G;
     const int qi = r / G;
+    // Q of unit `u`: this warp's 16 rows; returns their factors (lanes 0..15)
     auto load_q = [&](const TileUnit &u) -> float {
-      const bool valid = qi < u.npos;
-      const bf16 *qrow = p.q + static_cast<int64_t>(u.row0 + (valid ? qi : 0)) * p.q_stride +
-                         static_cast<int64_t>(u.kvh * G + g) * D;
-      const bool q16 = (reinterpret_cast<uintptr_t>(p.q) & 15u) == 0 && (p.q_stride & 7) == 0;
-      auto ldq = [&](int c) {
-        uint4 w = make_uint4(0u, 0u, 0u, 0u);
-        if (valid) {
-          if (q16) {
-            w = __ldg(reinterpret_cast<const uint4 *>(qrow) + c);
-          } else {
-            const uint32_t *q32 = reinterpret_cast<const uint32_t *>(qrow) + 4 * c;
-            w = make_uint4(__ldg(q32), __ldg(q32 + 1), __ldg(q32 + 2), __ldg(q32 + 3));
-          }
-        }
-        return w;
-      };
-      float rowf = 1.f;
-      float qmul = 1.f;
-      if constexpr (std::is_same<E, ElemBf16>::value) {
-        float amax = 0.f;
-#pragma unroll 4
-        for (int c = 0; c < D / 8; ++c) {
-          const uint4 w = ldq(c);
-          const uint32_t v[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-          for (int k = 0; k < 4; ++k)
-            amax = fmaxf(amax, fmaxf(fabsf(ElemBf16::lo(v[k])), fabsf(ElemBf16::hi(v[k]))));
-        }
-        const int ex = static_cast<int>((__float_as_uint(amax) >> 23) & 0xffu) - 127;
-        const int e = ex >= 15 ? min(ex - 14, 120) : 0;
-        qmul = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
-        rowf = __uint_as_float(static_cast<uint32_t>(127 + e) << 23);
-      }
-      constexpr int CQ = D / 16;  // this warp's half of the row's 16-byte chunks
-#pragma unroll 4
-      for (int c = part * CQ; c < (part + 1) * CQ; ++c) {
-        uint4 w = ldq(c);
-        if constexpr (std::is_same<E, ElemBf16>::value) {
-          w = make_uint4(ElemFp16::pack(ElemBf16::lo(w.x) * qmul, ElemBf16::hi(w.x) * qmul),
-                         ElemFp16::pack(ElemBf16::lo(w.y) * qmul, ElemBf16::hi(w.y) * qmul),
-                         ElemFp16::pack(ElemBf16::lo(w.z) * qmul, ElemBf16::hi(w.z) * qmul),
-                         ElemFp16::pack(ElemBf16::lo(w.w) * qmul, ElemBf16::hi(w.w) * qmul));
-        }
-        asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};\n" ::"r"(sQ + TL::off(r, c, Lay::Q_ATOM)),
-                     "r"(w.x), "r"(w.y), "r"(w.z), "r"(w.w)
-                     : "memory");
-      }
+      const float mine = load_q_rows<D, G, E>(p, u, 0, quad * 32 + part * 16, lane,
+                                              [&](int row, int c) { return sQ + TL::off(row, c, Lay::Q_ATOM); });
       fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) mbar_arrive(bar(Lay::B_QF));
-      return rowf;
+      return mine;
+    };
+    // the factors of this warp's 32 rows, from the lanes that stored their Q
+    auto row_factors = [&](float mine) -> float {
+      const float other = exchange(mine);
+      const float own = __shfl_sync(FULL, mine, lane & 15), got = __shfl_sync(FULL, other, lane & 15);
+      return (lane >> 4) == part ? own : got;
     };
 
     uint32_t ph = 0;
     TileUnit cur;
     read_unit(0, cur);
     float rowf = 1.f;  // the row's score factor: 2^e for a scaled bf16 row
-    if (!failed && !cur.stop) rowf = load_q(cur);
+    if (!failed && !cur.stop) rowf = row_factors(load_q(cur));
     for (uint32_t j = 0; !failed && !cur.stop; ++j) {
       const int nk = nranges(cur);
       const bool row_valid = qi < cur.npos;
@@ -1453,10 +1418,10 @@ __global__ void __launch_bounds__(kWideThreads, 1)
       if (failed) break;
       TileUnit nxt;
       read_unit(j + 1, nxt);
-      float nrowf = rowf;
+      float next_mine = 1.f;
       if (!failed && !nxt.stop) {
         wait_warp(bar(Lay::B_QE), j & 1u, failed);
-        if (!failed) nrowf = load_q(nxt);
+        if (!failed) next_mine = load_q(nxt);
       }
       if (failed) break;
       if (nk > 0) {
@@ -1499,8 +1464,8 @@ __global__ void __launch_bounds__(kWideThreads, 1)
         tc_fence_before();
       }
       ph += nk;
+      if (!nxt.stop) rowf = row_factors(next_mine);
       cur = nxt;
-      rowf = nrowf;
     }
   }
 
